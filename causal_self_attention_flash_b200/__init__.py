@@ -37,6 +37,9 @@ __all__ = [
     "attn_fwd_strided", "attn_bwd_strided", "split_qkv", "CausalAttentionQKV", "Layout",
     "Dropout", "dropout_params", "attn_dropout_mask_bytes", "attn_dropout_mask",
     "attn_decode", "attn_decode_workspace_bytes",
+    "attn_paged_plan", "attn_cache_append", "attn_decode_paged",
+    "attn_decode_paged_workspace_bytes", "attn_page_select", "attn_page_select_workspace_bytes",
+    "attn_decode_sparse",
     "SUPPORTED_HEAD_SIZES", "padded_head_size", "pad_qkv_projection", "pad_out_projection",
 ]
 
@@ -450,6 +453,189 @@ def attn_decode(q, k, v, L, scale=None, o=None, lse=None, workspace=None, stream
                          ws_ptr, ws_n, _stream(stream))
     _check("attn_decode", st)
     return o, lse
+
+
+def _array(t, dtype, shape, device, what):
+    """A contiguous device array of whole numbers or bounds; returns its
+    address."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} of shape {shape}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{what}: expected a tensor on {device}")
+    return t.data_ptr()
+
+
+def _table(t, B, device):
+    """A block table: int32 (B, width) with unit last stride; returns its
+    address, row stride and width."""
+    if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] != B or t.stride(1) != 1:
+        raise ValueError("block_table: expected an int32 (B, width) tensor with unit last stride")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"block_table: expected a tensor on {device}")
+    width = t.shape[1]
+    return t.data_ptr(), t.stride(0) if B > 1 else width, width
+
+
+def _cache(k, v, D, device):
+    """(n_pages, Hkv, page_size) and layouts of the cache views."""
+    lk = _layout(k, torch.bfloat16, "k_cache", None, device)
+    lv = _layout(v, torch.bfloat16, "v_cache", k.shape, device)
+    n_pages, Hkv, P, Dk = k.shape
+    if Dk != D:
+        raise ValueError(f"k_cache: head size {Dk}, expected {D}")
+    return n_pages, Hkv, P, lk, lv
+
+
+def attn_paged_plan(new_tokens, lengths, block_table, free_ring, ring_state, page_size, n_slots,
+                    lengths_out=None, ring_state_out=None, cu_new=None, slots=None,
+                    positions=None, status=None, stream=None):
+    """Pages, slots and positions of a step's new tokens (see
+    include/cattn.h): new_tokens, lengths int32 (B), block_table int32
+    (B, width) and free_ring int32 (n_pages) updated in place, ring_state
+    int64 (2).  Returns (lengths_out, ring_state_out, cu_new, slots,
+    positions, status), all on the device; lengths_out and ring_state_out may
+    be lengths and ring_state.  status is 0, or why nothing was changed."""
+    dev = new_tokens.device
+    B, n_pages = new_tokens.numel(), free_ring.numel()
+    i32, i64 = torch.int32, torch.int64
+    n_slots = int(n_slots)
+    if n_slots < 0:
+        raise ValueError("n_slots must not be negative")
+    p_new = _array(new_tokens, i32, (B,), dev, "new_tokens")
+    p_len = _array(lengths, i32, (B,), dev, "lengths")
+    p_table, stride, width = _table(block_table, B, dev)
+    p_ring = _array(free_ring, i32, (n_pages,), dev, "free_ring")
+    p_state = _array(ring_state, i64, (2,), dev, "ring_state")
+    _same_device(new_tokens)
+    lengths_out = _want(lengths_out, new_tokens, i32, (B,))
+    ring_state_out = _want(ring_state_out, new_tokens, i64, (2,))
+    cu_new = _want(cu_new, new_tokens, i32, (B + 1,))
+    slots = _want(slots, new_tokens, i64, (n_slots,))
+    positions = _want(positions, new_tokens, i32, (n_slots,))
+    status = _want(status, new_tokens, i32, (1,))
+    st = LIB.attn_paged_plan(p_new, p_len, p_table, stride, p_ring, p_state, B, width, n_pages,
+                             int(page_size), n_slots, lengths_out.data_ptr(),
+                             ring_state_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+                             positions.data_ptr(), status.data_ptr(), _stream(stream))
+    _check("attn_paged_plan", st)
+    return lengths_out, ring_state_out, cu_new, slots, positions, status
+
+
+def attn_cache_append(k_new, v_new, k_cache, v_cache, slots, bounds=None, stream=None):
+    """Writes the rows of k_new and v_new, bf16 (n, Hkv, D) views, into the
+    cache rows slots, int64 (n); negative ones are skipped.  k_cache, v_cache
+    bf16 (n_pages, Hkv, page_size, D) views.  bounds, bf16 (n_pages, Hkv, 2,
+    D): the pages' lowest and highest key values, kept up to date for
+    attn_page_select."""
+    n, Hn, D = k_new.shape
+    dev = k_new.device
+    n_pages, Hkv, P, lk, lv = _cache(k_cache, v_cache, D, dev)
+    if Hn != Hkv or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new, v_new: expected (n, {Hkv}, {D})")
+    for t, what in ((k_new, "k_new"), (v_new, "v_new")):
+        if t.dtype != torch.bfloat16 or t.stride(2) != 1 or not t.is_cuda or t.device != dev:
+            raise ValueError(f"{what}: expected a bf16 view on {dev} with unit last stride")
+    p_slots = _array(slots, torch.int64, (n,), dev, "slots")
+    p_bounds = None
+    if bounds is not None:
+        p_bounds = _array(bounds, torch.bfloat16, (n_pages, Hkv, 2, D), dev, "bounds")
+    _same_device(k_new)
+    st = LIB.attn_cache_append(k_new.data_ptr(), Layout(8, k_new.stride(1), k_new.stride(0)),
+                               v_new.data_ptr(), Layout(8, v_new.stride(1), v_new.stride(0)),
+                               n, Hkv, D, n_pages, P, p_slots, k_cache.data_ptr(), lk,
+                               v_cache.data_ptr(), lv, p_bounds, _stream(stream))
+    _check("attn_cache_append", st)
+
+
+def attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D):
+    return int(LIB.attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D))
+
+
+def _decode_paged(name, q, k_cache, v_cache, block_table, lengths, pages, scale, o, lse,
+                  workspace, stream):
+    B, H, Tq, D = _shape(q)
+    dev = q.device
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    lq = _layout(q, torch.bfloat16, "q", None, dev)
+    n_pages, Hkv, P, lk, lv = _cache(k_cache, v_cache, D, dev)
+    p_table, stride, width = _table(block_table, B, dev)
+    p_len = _array(lengths, torch.int32, (B,), dev, "lengths")
+    listed = ()
+    if pages is not None:
+        K = pages.shape[-1]
+        listed = (_array(pages, torch.int32, (B, Hkv, K), dev, "pages"), K)
+    _same_device(q)
+    if o is None:
+        o = torch.empty((B, H, Tq, D), dtype=torch.bfloat16, device=dev)
+    lo = _layout(o, torch.bfloat16, "o", (B, H, Tq, D), dev)
+    lse = _want(lse, q, torch.float32, (B, H, Tq))
+    if workspace is None:
+        workspace = _workspace(None, q, attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D))
+    else:
+        _workspace(workspace, q, 0)
+    st = getattr(LIB, name)(q.data_ptr(), lq, k_cache.data_ptr(), lk, v_cache.data_ptr(), lv,
+                            float(scale), B, H, Hkv, Tq, D, n_pages, P, p_table, stride, width,
+                            p_len, *listed, o.data_ptr(), lo, lse.data_ptr(),
+                            workspace.data_ptr(), _nbytes(workspace), _stream(stream))
+    _check(name, st)
+    return o, lse
+
+
+def attn_decode_paged(q, k_cache, v_cache, block_table, lengths, scale=None, o=None, lse=None,
+                      workspace=None, stream=None):
+    """Attention of the Tq newest positions of B requests against their pages
+    of a paged cache: q bf16 (B, H, Tq, D) holds the rows at positions
+    lengths[b] - Tq .. lengths[b] - 1, k_cache and v_cache bf16 (n_pages, Hkv,
+    page_size, D) views, block_table int32 (B, width), lengths int32 (B) on
+    the device.  Returns (o, lse), o (B, H, Tq, D) bf16 and lse (B, H, Tq)
+    fp32; rows that see no key give 0 and -inf.  workspace: a uint8 CUDA
+    tensor of attn_decode_paged_workspace_bytes bytes, allocated if not
+    given."""
+    return _decode_paged("attn_decode_paged", q, k_cache, v_cache, block_table, lengths, None,
+                         scale, o, lse, workspace, stream)
+
+
+def attn_decode_sparse(q, k_cache, v_cache, block_table, lengths, pages, scale=None, o=None,
+                       lse=None, workspace=None, stream=None):
+    """attn_decode_paged over the listed pages only: pages int32 (B, Hkv, K)
+    as attn_page_select gives them."""
+    return _decode_paged("attn_decode_sparse", q, k_cache, v_cache, block_table, lengths, pages,
+                         scale, o, lse, workspace, stream)
+
+
+def attn_page_select_workspace_bytes(B, Hkv, width):
+    return int(LIB.attn_page_select_workspace_bytes(B, Hkv, width))
+
+
+def attn_page_select(q, bounds, block_table, lengths, page_size, n_select, n_first=1, n_last=1,
+                     pages=None, workspace=None, stream=None):
+    """The n_select pages of each request and cache head whose channel bounds
+    (see attn_cache_append) promise the largest scores for the query rows q
+    bf16 (B, H, Tq, D), the n_first first and n_last last among them; int32
+    (B, Hkv, n_select), ascending, -1 behind the last."""
+    B, H, Tq, D = _shape(q)
+    dev = q.device
+    lq = _layout(q, torch.bfloat16, "q", None, dev)
+    if bounds.dim() != 4:
+        raise ValueError("bounds: expected (n_pages, Hkv, 2, D)")
+    n_pages, Hkv = bounds.shape[0], bounds.shape[1]
+    p_bounds = _array(bounds, torch.bfloat16, (n_pages, Hkv, 2, D), dev, "bounds")
+    p_table, stride, width = _table(block_table, B, dev)
+    p_len = _array(lengths, torch.int32, (B,), dev, "lengths")
+    _same_device(q)
+    pages = _want(pages, q, torch.int32, (B, Hkv, int(n_select)))
+    if workspace is None:
+        workspace = _workspace(None, q, attn_page_select_workspace_bytes(B, Hkv, width))
+    else:
+        _workspace(workspace, q, 0)
+    st = LIB.attn_page_select(q.data_ptr(), lq, p_bounds, B, H, Hkv, Tq, D, n_pages,
+                              int(page_size), p_table, stride, width, p_len, int(n_select),
+                              int(n_first), int(n_last), pages.data_ptr(), workspace.data_ptr(),
+                              _nbytes(workspace), _stream(stream))
+    _check("attn_page_select", st)
+    return pages
 
 
 SUPPORTED_HEAD_SIZES = (16, 32, 64, 128)

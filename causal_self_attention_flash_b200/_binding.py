@@ -41,6 +41,7 @@ class Dropout(ctypes.Structure):
 # name -> (restype, argtypes), mirroring include/cattn.h
 _vp, _i, _f, _sz, _u32 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
                           ctypes.c_size_t, ctypes.c_uint32)
+_ll = ctypes.c_longlong
 _L = Layout
 _DP = ctypes.POINTER(Dropout)
 SIGNATURES = {
@@ -66,6 +67,18 @@ SIGNATURES = {
     "attn_dropout_mask_bytes": (_sz, [_i, _i, _i]),
     "attn_decode": (_i, [_vp, _L, _vp, _L, _vp, _L, _f, _i, _i, _i, _i, _i, _vp, _L, _vp, _vp,
                          _sz, _vp]),
+    "attn_paged_plan": (_i, [_vp, _vp, _vp, _ll, _vp, _vp, _i, _i, _i, _i, _ll, _vp, _vp, _vp, _vp,
+                             _vp, _vp, _vp]),
+    "attn_cache_append": (_i, [_vp, _L, _vp, _L, _ll, _i, _i, _i, _i, _vp, _vp, _L, _vp, _L, _vp,
+                               _vp]),
+    "attn_decode_paged_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "attn_decode_paged": (_i, [_vp, _L, _vp, _L, _vp, _L, _f, _i, _i, _i, _i, _i, _i, _i, _vp, _ll,
+                               _i, _vp, _vp, _L, _vp, _vp, _sz, _vp]),
+    "attn_page_select_workspace_bytes": (_sz, [_i, _i, _i]),
+    "attn_page_select": (_i, [_vp, _L, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _ll, _i, _vp, _i, _i,
+                              _i, _vp, _vp, _sz, _vp]),
+    "attn_decode_sparse": (_i, [_vp, _L, _vp, _L, _vp, _L, _f, _i, _i, _i, _i, _i, _i, _i, _vp,
+                                _ll, _i, _vp, _vp, _i, _vp, _L, _vp, _vp, _sz, _vp]),
     "cattn_get_device_status": (_i, [_i, _vp]),
     "cattn_set_wait_timeout_us": (None, [_u32]),
     "cattn_selftest_wait_timeout": (_i, [_u32, _vp]),

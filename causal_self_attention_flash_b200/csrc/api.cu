@@ -17,6 +17,8 @@
 #include "bwd.cuh"
 #include "decode.cuh"
 #include "fwd.cuh"
+#include "paged_cache.cuh"
+#include "paged_decode.cuh"
 
 // Scratch of attn_bwd_noalloc: one fixed array per device, owned by the
 // library for the process's lifetime.  Host code must not use this name as
@@ -354,7 +356,8 @@ int grid_for(size_t work_items, int per_block) {
 // benchmarking aid; off by default, and then it costs nothing).
 
 enum KernelId {
-  K_FWD = 0, K_BWD_PRE = 1, K_BWD_MAIN = 2, K_DQ_CONVERT = 3, K_DECODE = 4, K_COUNT = 5
+  K_FWD = 0, K_BWD_PRE = 1, K_BWD_MAIN = 2, K_DQ_CONVERT = 3, K_DECODE = 4, K_CACHE = 5,
+  K_SELECT = 6, K_COUNT = 7
 };
 
 bool g_timing = false;
@@ -725,6 +728,135 @@ cattn_status decode_impl(const DecodeParams& p, long long BH, int dev, cudaStrea
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 
+// ------------------------------------------------------------ paged cache
+
+// Shape checks that the calls on a paged cache share.
+cattn_status check_paged(int B, int H, int Hkv, int D, int n_pages, int P, int width) {
+  const cattn_status st = check_shape(B, H, 1, D);
+  if (st != CATTN_OK) return st;
+  if (Hkv < 1 || H % Hkv != 0 || n_pages < 1 || P < 1 || width < 1) return CATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(width) * P > (1LL << 30)) return CATTN_ERR_INVALID_ARG;
+  return CATTN_OK;
+}
+
+template <int D, bool UP>
+cattn_status paged_impl(const PagedParams& p, int grid, int dev, cudaStream_t s) {
+  cattn_status st = ensure_smem(dev, 68 + 2 * d_index(D) + UP, paged_decode_kernel<D, UP>,
+                                paged_smem_bytes(D));
+  if (st != CATTN_OK) return st;
+  clear_stale_error();
+  LaunchTimer t(K_DECODE, s);
+  cudaError_t e = launch_dependent(true, paged_decode_kernel<D, UP>, dim3(grid),
+                                   dim3(kPagedThreads), paged_smem_bytes(D), s, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(true, paged_merge_kernel<D>, dim3(grid * kPagedWarps),
+                         dim3(kMergeThreads), paged_merge_smem_bytes(D), s, p);
+  return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
+}
+
+// attn_decode_paged (pages == nullptr) and attn_decode_sparse.
+cattn_status paged_decode(const void* q, cattn_layout lq, const void* k, cattn_layout lk,
+                          const void* v, cattn_layout lv, float scale, int B, int H, int Hkv,
+                          int Tq, int D, int n_pages, int P, const int32_t* table,
+                          long long table_stride, int width, const int32_t* lengths,
+                          const int32_t* pages, int n_sel, void* o, cattn_layout lo, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  cattn_status st = check_paged(B, H, Hkv, D, n_pages, P, width);
+  if (st != CATTN_OK) return st;
+  if (!(scale > 0.f) || !isfinite(scale)) return CATTN_ERR_INVALID_ARG;
+  if (Tq > kDecodeMaxTq) return CATTN_ERR_UNSUPPORTED;
+  if (Tq < 1) return CATTN_ERR_INVALID_ARG;
+  if (B == 0 || H == 0) return CATTN_OK;
+  if (!q || !k || !v || !o || !lse || !table || !lengths || !workspace)
+    return CATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+      !aligned(lse, 4) || !aligned(table, 4) || !aligned(lengths, 4) || !aligned(pages, 4) ||
+      !aligned(workspace, 256))
+    return CATTN_ERR_INVALID_ARG;
+  if (!layout_ok(lq) || !layout_ok(lk) || !layout_ok(lv) || !layout_ok(lo))
+    return CATTN_ERR_INVALID_ARG;
+  if (!output_layout_ok(lo, B, H, Tq, D)) return CATTN_ERR_INVALID_ARG;
+  if (table_stride < width) return CATTN_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(H / Hkv) * Tq;
+  const long long keys = static_cast<long long>(pages ? n_sel : width) * P;
+  if (keys > (1LL << 30) || rows > (1LL << 20)) return CATTN_ERR_INVALID_ARG;
+  const long long chunks = (keys + paged_chunk(D) - 1) / paged_chunk(D);
+  if (B * chunks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
+  PagedParams p;
+  p.rows = static_cast<int>(rows);
+  p.n_tiles = (p.rows + kPagedRows - 1) / kPagedRows;
+  p.R = p.rows < kPagedRows ? p.rows : kPagedRows;
+  if (workspace_bytes < static_cast<size_t>(paged_workspace_bytes(p.R, D)))
+    return CATTN_ERR_INVALID_ARG;
+  int dev;
+  if ((st = check_device(&dev)) != CATTN_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_sb = lq.b; p.q_sh = lq.h; p.q_st = lq.t;
+  p.k_sp = lk.b; p.k_sh = lk.h; p.k_st = lk.t;
+  p.v_sp = lv.b; p.v_sh = lv.h; p.v_st = lv.t;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_sb = lo.b; p.o_sh = lo.h; p.o_st = lo.t;
+  p.lse = lse;
+  p.table = table;
+  p.table_sb = table_stride;
+  p.lengths = lengths;
+  p.pages = pages;
+  p.B = B; p.H = H; p.Hkv = Hkv; p.Tq = Tq;
+  p.n_pages = n_pages; p.P = P; p.width = width; p.n_sel = n_sel;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.cuts = reinterpret_cast<PagedCut*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + paged_ml_offset());
+  p.part_o = reinterpret_cast<float*>(ws + paged_o_offset(p.R));
+  // one resident wave, or as many CTAs as the table's width can fill
+  long long grid = B * chunks * Hkv * p.n_tiles;
+  grid = (grid / kPagedMinRun + kPagedWarps) / kPagedWarps;
+  long long slots = 2LL * g_sm_count[dev];
+  if (slots > kPagedMaxCtas) slots = kPagedMaxCtas;
+  if (grid > slots) grid = slots;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int gr = static_cast<int>(grid);
+  const bool up = p.rows > 8;
+  switch (D) {
+    case 16: return up ? paged_impl<16, true>(p, gr, dev, s) : paged_impl<16, false>(p, gr, dev, s);
+    case 32: return up ? paged_impl<32, true>(p, gr, dev, s) : paged_impl<32, false>(p, gr, dev, s);
+    case 64: return up ? paged_impl<64, true>(p, gr, dev, s) : paged_impl<64, false>(p, gr, dev, s);
+    case 128:
+      return up ? paged_impl<128, true>(p, gr, dev, s) : paged_impl<128, false>(p, gr, dev, s);
+  }
+  return CATTN_ERR_UNSUPPORTED;
+}
+
+template <int D>
+cattn_status append_impl(const AppendParams& p, cudaStream_t s) {
+  const long long blocks = (p.n * p.Hkv * (D / 8) + kAppendThreads - 1) / kAppendThreads;
+  if (blocks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
+  clear_stale_error();
+  LaunchTimer t(K_CACHE, s);
+  const dim3 g(static_cast<unsigned>(blocks));
+  const cudaError_t e =
+      p.bounds ? launch_dependent(true, cache_append_kernel<D, true>, g, dim3(kAppendThreads), 0, s, p)
+               : launch_dependent(true, cache_append_kernel<D, false>, g, dim3(kAppendThreads), 0, s, p);
+  return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
+}
+
+template <int D>
+cattn_status select_impl(const SelectParams& p, cudaStream_t s) {
+  const long long bh = static_cast<long long>(p.B) * p.Hkv;
+  clear_stale_error();
+  LaunchTimer t(K_SELECT, s);
+  cudaError_t e = cudaSuccess;
+  if (p.width > p.n_sel)  // (else every page is taken)
+    e = launch_dependent(true, page_score_kernel<D>, dim3(static_cast<unsigned>(bh * p.n_blocks)),
+                         dim3(kScoreThreads), 0, s, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(true, page_pick_kernel, dim3(static_cast<unsigned>(bh)),
+                         dim3(kPickThreads), pick_smem_bytes(), s, p);
+  return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
+}
+
 }  // namespace
 }  // namespace cattn
 
@@ -842,6 +974,202 @@ cattn_status attn_decode(const void* q, cattn_layout lq, const void* k, cattn_la
     case 32: return decode_impl<32>(p, BH, dev, s);
     case 64: return decode_impl<64>(p, BH, dev, s);
     case 128: return decode_impl<128>(p, BH, dev, s);
+  }
+  return CATTN_ERR_UNSUPPORTED;
+}
+
+size_t attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int Tq, int D) {
+  if (check_paged(B, H, Hkv, D, 1, 1, 1) != CATTN_OK || Tq < 1 || Tq > kDecodeMaxTq) return 0;
+  if (B == 0 || H == 0) return 0;
+  const long long rows = static_cast<long long>(H / Hkv) * Tq;
+  return static_cast<size_t>(
+      paged_workspace_bytes(rows < kPagedRows ? static_cast<int>(rows) : kPagedRows, D));
+}
+
+cattn_status attn_decode_paged(const void* q, cattn_layout lq, const void* k_cache,
+                               cattn_layout lk, const void* v_cache, cattn_layout lv, float scale,
+                               int B, int H, int Hkv, int Tq, int D, int n_pages, int page_size,
+                               const int32_t* block_table, long long table_stride, int width,
+                               const int32_t* lengths, void* o, cattn_layout lo, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_decode(q, lq, k_cache, lk, v_cache, lv, scale, B, H, Hkv, Tq, D, n_pages,
+                      page_size, block_table, table_stride, width, lengths, nullptr, 0, o, lo, lse,
+                      workspace, workspace_bytes, stream);
+}
+
+cattn_status attn_decode_sparse(const void* q, cattn_layout lq, const void* k_cache,
+                                cattn_layout lk, const void* v_cache, cattn_layout lv, float scale,
+                                int B, int H, int Hkv, int Tq, int D, int n_pages, int page_size,
+                                const int32_t* block_table, long long table_stride, int width,
+                                const int32_t* lengths, const int32_t* pages, int n_select,
+                                void* o, cattn_layout lo, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (n_select < 1) return CATTN_ERR_INVALID_ARG;
+  if (!pages && B > 0 && H > 0) return CATTN_ERR_INVALID_ARG;
+  return paged_decode(q, lq, k_cache, lk, v_cache, lv, scale, B, H, Hkv, Tq, D, n_pages,
+                      page_size, block_table, table_stride, width, lengths, pages, n_select, o, lo,
+                      lse, workspace, workspace_bytes, stream);
+}
+
+cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, const void* v_new,
+                               cattn_layout lvn, long long n, int Hkv, int D, int n_pages,
+                               int page_size, const int64_t* slots, void* k_cache,
+                               cattn_layout lk, void* v_cache, cattn_layout lv, void* bounds,
+                               void* stream) {
+  cattn_status st = check_paged(1, Hkv, Hkv, D, n_pages, page_size, 1);
+  if (st != CATTN_OK) return st;
+  if (n < 0) return CATTN_ERR_INVALID_ARG;
+  if (n == 0) return CATTN_OK;
+  if (!k_new || !v_new || !slots || !k_cache || !v_cache) return CATTN_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(bounds, 16))
+    return CATTN_ERR_INVALID_ARG;
+  lkn.b = lkn.t;  // rows are one axis: no batch stride
+  lvn.b = lvn.t;
+  if (!layout_ok(lkn) || !layout_ok(lvn) || !layout_ok(lk) || !layout_ok(lv))
+    return CATTN_ERR_INVALID_ARG;
+  if (!output_layout_ok(lk, n_pages, Hkv, page_size, D) ||
+      !output_layout_ok(lv, n_pages, Hkv, page_size, D))
+    return CATTN_ERR_INVALID_ARG;
+  int dev;
+  if ((st = check_device(&dev)) != CATTN_OK) return st;
+  AppendParams p;
+  p.kn = static_cast<const __nv_bfloat16*>(k_new);
+  p.vn = static_cast<const __nv_bfloat16*>(v_new);
+  p.kn_st = lkn.t; p.kn_sh = lkn.h; p.vn_st = lvn.t; p.vn_sh = lvn.h;
+  p.k = static_cast<__nv_bfloat16*>(k_cache);
+  p.v = static_cast<__nv_bfloat16*>(v_cache);
+  p.k_sp = lk.b; p.k_sh = lk.h; p.k_st = lk.t;
+  p.v_sp = lv.b; p.v_sh = lv.h; p.v_st = lv.t;
+  p.slots = reinterpret_cast<const long long*>(slots);
+  p.bounds = static_cast<__nv_bfloat16*>(bounds);
+  p.n = n;
+  p.Hkv = Hkv;
+  p.P = page_size;
+  p.n_rows = static_cast<long long>(n_pages) * page_size;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (D) {
+    case 16: return append_impl<16>(p, s);
+    case 32: return append_impl<32>(p, s);
+    case 64: return append_impl<64>(p, s);
+    case 128: return append_impl<128>(p, s);
+  }
+  return CATTN_ERR_UNSUPPORTED;
+}
+
+cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
+                             int32_t* block_table, long long table_stride, int32_t* free_ring,
+                             const int64_t* ring_state, int B, int width, int n_pages,
+                             int page_size, long long n_slots, int32_t* lengths_out,
+                             int64_t* ring_state_out, int32_t* cu_new, int64_t* slots,
+                             int32_t* positions, int32_t* status, void* stream) {
+  cattn_status st = check_paged(B, 1, 1, 16, n_pages, page_size, width);
+  if (st != CATTN_OK) return st;
+  if (B > kPlanMaxB) return CATTN_ERR_UNSUPPORTED;
+  if (n_slots < 0 || n_slots > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
+  if (table_stride < width) return CATTN_ERR_INVALID_ARG;
+  if (!free_ring || !ring_state || !ring_state_out || !cu_new || !status)
+    return CATTN_ERR_INVALID_ARG;
+  if (B > 0 && (!new_tokens || !lengths || !block_table || !lengths_out))
+    return CATTN_ERR_INVALID_ARG;
+  if (n_slots > 0 && (!slots || !positions)) return CATTN_ERR_INVALID_ARG;
+  if (!aligned(new_tokens, 4) || !aligned(lengths, 4) || !aligned(block_table, 4) ||
+      !aligned(free_ring, 4) || !aligned(ring_state, 8) || !aligned(lengths_out, 4) ||
+      !aligned(ring_state_out, 8) || !aligned(cu_new, 4) || !aligned(slots, 8) ||
+      !aligned(positions, 4) || !aligned(status, 4))
+    return CATTN_ERR_INVALID_ARG;
+  int dev;
+  if ((st = check_device(&dev)) != CATTN_OK) return st;
+  if ((st = ensure_smem(dev, 76, paged_plan_kernel, plan_smem_bytes(kPlanMaxB))) != CATTN_OK)
+    return st;
+  PlanParams p;
+  p.asked = new_tokens;
+  p.lengths = lengths;
+  p.table = block_table;
+  p.table_sb = table_stride;
+  p.ring = free_ring;
+  p.state = reinterpret_cast<const long long*>(ring_state);
+  p.B = B; p.width = width; p.n_pages = n_pages; p.P = page_size;
+  p.n_slots = n_slots;
+  p.lengths_out = lengths_out;
+  p.state_out = reinterpret_cast<long long*>(ring_state_out);
+  p.cu = cu_new;
+  p.slots = reinterpret_cast<long long*>(slots);
+  p.positions = positions;
+  p.status = status;
+  // a CTA per kPlanThreads slots or requests, as far as one cluster goes
+  long long n = (n_slots > B ? n_slots : B) / kPlanThreads + 1;
+  if (n > kPlanMaxCtas) n = kPlanMaxCtas;
+  clear_stale_error();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n));
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = plan_smem_bytes(B);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(n);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = n > 1 ? 2 : 1;
+  LaunchTimer t(K_CACHE, cfg.stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, p, static_cast<int>(n));
+  return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
+}
+
+size_t attn_page_select_workspace_bytes(int B, int Hkv, int width) {
+  if (B <= 0 || Hkv <= 0 || width <= 0) return 0;
+  return static_cast<size_t>(B) * Hkv * width * sizeof(double);
+}
+
+cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds, int B, int H,
+                              int Hkv, int Tq, int D, int n_pages, int page_size,
+                              const int32_t* block_table, long long table_stride, int width,
+                              const int32_t* lengths, int n_select, int n_first, int n_last,
+                              int32_t* pages, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  cattn_status st = check_paged(B, H, Hkv, D, n_pages, page_size, width);
+  if (st != CATTN_OK) return st;
+  if (Tq > kDecodeMaxTq) return CATTN_ERR_UNSUPPORTED;
+  if (Tq < 1 || n_select < 1 || n_first < 0 || n_last < 0 || n_first > n_select ||
+      n_last > n_select - n_first)
+    return CATTN_ERR_INVALID_ARG;
+  if (B == 0 || H == 0) return CATTN_OK;
+  if (!q || !bounds || !block_table || !lengths || !pages) return CATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(block_table, 4) ||
+      !aligned(lengths, 4) || !aligned(pages, 4) || !aligned(workspace, 256))
+    return CATTN_ERR_INVALID_ARG;
+  if (!layout_ok(lq) || table_stride < width) return CATTN_ERR_INVALID_ARG;
+  if (width > n_select &&
+      (!workspace || workspace_bytes < attn_page_select_workspace_bytes(B, Hkv, width)))
+    return CATTN_ERR_INVALID_ARG;
+  SelectParams p;
+  p.n_blocks = (width + kScorePages - 1) / kScorePages;
+  const long long bh = static_cast<long long>(B) * Hkv;
+  if (bh * p.n_blocks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
+  int dev;
+  if ((st = check_device(&dev)) != CATTN_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_sb = lq.b; p.q_sh = lq.h; p.q_st = lq.t;
+  p.bounds = static_cast<const __nv_bfloat16*>(bounds);
+  p.table = block_table;
+  p.table_sb = table_stride;
+  p.lengths = lengths;
+  p.B = B; p.H = H; p.Hkv = Hkv; p.Tq = Tq;
+  p.rows = H / Hkv * Tq;
+  p.n_pages = n_pages; p.P = page_size; p.width = width;
+  p.n_sel = n_select; p.n_first = n_first; p.n_last = n_last;
+  p.pages = pages;
+  p.score = static_cast<double*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (D) {
+    case 16: return select_impl<16>(p, s);
+    case 32: return select_impl<32>(p, s);
+    case 64: return select_impl<64>(p, s);
+    case 128: return select_impl<128>(p, s);
   }
   return CATTN_ERR_UNSUPPORTED;
 }

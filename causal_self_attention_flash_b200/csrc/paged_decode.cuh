@@ -1,0 +1,614 @@
+// Decode attention over a paged key/value cache.
+//
+// As decode.cuh (the newest Tq positions of a sequence against its cached
+// keys and values), for many sequences of different lengths whose keys lie
+// in pages of a common pool: request b's position p is row p % P of page
+// table[b][p / P].  H query heads read Hkv cache heads, G = H / Hkv query
+// heads each.  For the query row at position x = len - Tq + t:
+//
+//   s_j = scale q . k_j,  o = sum_j exp(s_j) v_j / sum_j exp(s_j),
+//   lse = log sum_j exp(s_j)   over the held keys j <= x
+//
+// (o = 0 and lse = -inf where no key is held).  The sparse form reads the
+// keys of K listed pages per (request, cache head) only.
+//
+// The bound is reading K and V once (4 D bytes per key and cache head for
+// 4 D G Tq flops), so the design is about a steady read by every SM however
+// the lengths are spread:
+//   - the keys of every item (request, cache head, tile of <= 16 query rows)
+//     are cut into chunks of paged_chunk(D) keys; all items' chunks in a row
+//     form one flat axis that is dealt evenly to the warps of one resident
+//     wave, each a contiguous run.  Lengths live on the GPU, so every CTA
+//     works out the cuts itself, from one scan of the lengths;
+//   - a warp streams its run through a private ring of kPagedStages shared
+//     memory slots with cp.async, on across items; per chunk it multiplies
+//     q k^T and p v with mma.sync m16n8k16 (query rows as the A operand, at
+//     most 16) and keeps the running maximum and sum (online softmax);
+//   - an item that ends inside its warp's run is written out directly; a cut
+//     item leaves (m, l, o) per warp in the workspace and merge_kernel joins
+//     them, in the order of the keys, so results repeat bit for bit.
+// p enters the second product as a bf16 pair (hi + lo, about 16 bits): the
+// tensor pipe has room (the kernel waits for memory), and o then carries no
+// rounding but its own to bf16.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#ifndef CATTN_HOST_EMULATION
+#include "paged_ptx.cuh"
+#endif
+
+namespace cattn {
+
+constexpr int kPagedWarps = 4;                    // warps per CTA
+constexpr int kPagedThreads = 32 * kPagedWarps;
+constexpr int kPagedStages = 3;                   // chunks in flight per warp
+constexpr int kPagedMaxCtas = 2 * 148;            // resident CTAs of a B200 (2 x 99 KB)
+constexpr int kPagedMaxWarps = kPagedMaxCtas * kPagedWarps;
+constexpr int kPagedMinRun = 2;                   // chunks that a warp takes at least
+constexpr int kPagedRows = 16;                    // query rows per item
+constexpr int kPagedNone = 0x7fffffff;            // position of a key that is not held
+constexpr int kMergeThreads = 256;
+
+// Keys per chunk: 4 KB of K and 4 KB of V at D >= 64; at most 32, one lane
+// per key.
+__host__ __device__ constexpr int paged_chunk(int D) { return D == 128 ? 16 : 32; }
+__host__ __device__ constexpr int paged_chunk_bytes(int D) { return paged_chunk(D) * D * 4; }
+__host__ __device__ constexpr int paged_ring_bytes(int D) {
+  return kPagedWarps * kPagedStages * paged_chunk_bytes(D);
+}
+// Dynamic shared memory: the rings, the key positions of their slots, the
+// scan's prefix sums and warp totals.
+__host__ __device__ constexpr int paged_smem_bytes(int D) {
+  return paged_ring_bytes(D) + kPagedWarps * kPagedStages * 32 * 4 + (kPagedThreads + 8) * 4;
+}
+
+// Where a cut item begins: its partial results are slot 1 of warp w and
+// slot 0 of the n_parts - 1 warps behind it (n_parts = 0: none begins in w).
+struct PagedCut {
+  int b, ht, n_parts, pad;
+};
+
+// Workspace: PagedCut[kPagedMaxWarps], then (m, l) and o of two slots per
+// warp with R = min(16, G Tq) rows each.
+__host__ __device__ constexpr long long paged_ml_offset() {
+  return static_cast<long long>(kPagedMaxWarps) * static_cast<long long>(sizeof(PagedCut));
+}
+__host__ __device__ constexpr long long paged_o_offset(int R) {
+  return paged_ml_offset() + 2LL * kPagedMaxWarps * R * 8;
+}
+__host__ __device__ constexpr long long paged_workspace_bytes(int R, int D) {
+  return paged_o_offset(R) + 2LL * kPagedMaxWarps * R * D * 4;
+}
+
+struct PagedParams {
+  const __nv_bfloat16* q;  // (B, H, Tq, D)
+  const __nv_bfloat16* k;  // (n_pages, Hkv, P, D)
+  const __nv_bfloat16* v;
+  long long q_sb, q_sh, q_st, k_sp, k_sh, k_st, v_sp, v_sh, v_st;
+  __nv_bfloat16* o;        // (B, H, Tq, D)
+  long long o_sb, o_sh, o_st;
+  float* lse;              // (B, H, Tq) contiguous, natural log
+  const int* table;        // (B, width), row stride table_sb
+  long long table_sb;
+  const int* lengths;      // (B)
+  const int* pages;        // (B, Hkv, n_sel) logical pages, or null: all
+  int B, H, Hkv, Tq, rows; // rows = G Tq
+  int n_tiles;             // ceil(rows / 16)
+  int n_pages, P, width, n_sel;
+  int R;                   // rows of a partial slot, min(16, rows)
+  float scale_log2;        // scale * log2(e)
+  PagedCut* cuts;
+  float2* part_ml;         // [2 warps][R]
+  float* part_o;           // [2 warps][R][D]
+};
+
+// Keys of request b that its items enumerate (sparse: of the listed pages),
+// and the chunks they take; an item without keys has one, empty, chunk.
+__device__ __forceinline__ int paged_keys(const PagedParams& p, int len) {
+  if (len < 0) len = 0;
+  if (p.pages != nullptr) {
+    const int have = len / p.P + (len % p.P != 0);
+    return (have < p.n_sel ? have : p.n_sel) * p.P;
+  }
+  const int cap = p.width * p.P;
+  return len < cap ? len : cap;
+}
+template <int D>
+__device__ __forceinline__ int paged_chunks(const PagedParams& p, int len) {
+  const int n = (paged_keys(p, len) + paged_chunk(D) - 1) / paged_chunk(D);
+  return n > 0 ? n : 1;
+}
+
+// A place on the flat axis: chunk c of the n of item (b, ht).
+struct PagedPlace {
+  int b, ht, c, n, len;
+};
+
+template <int D>
+__device__ __forceinline__ void paged_next(const PagedParams& p, int HT, PagedPlace& x) {
+  if (++x.c < x.n) return;
+  x.c = 0;
+  if (++x.ht < HT) return;
+  x.ht = 0;
+  if (++x.b >= p.B) return;  // behind the last item
+  x.len = p.lengths[x.b];
+  x.n = paged_chunks<D>(p, x.len);
+}
+
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int u = dec_shfl(v, lane >= d ? lane - d : 0);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// The place of flat chunk x: request b holds chunks HT * before(b) up to
+// HT * before(b + 1), before = the chunks of one head of the requests in
+// front.  pre[t] is before(t * nb).  (The lengths are read again here; the
+// clamps keep every index in range should a caller change them meanwhile.)
+template <int D>
+__device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT, int nb,
+                                                   const int* pre, long long x, int lane) {
+  const int y = static_cast<int>(x / HT);
+  int t = -1;  // pre[0] = 0 <= y: at least 0 in the end
+#pragma unroll
+  for (int i = 0; i < kPagedThreads / 32; ++i) t += dec_popc(dec_ballot(pre[32 * i + lane] <= y));
+  int run = pre[t];
+  for (int b0 = t * nb; b0 < (t + 1) * nb; b0 += 32) {
+    const int b = b0 + lane;
+    const bool in = lane < (t + 1) * nb - b0 && b < p.B;
+    const int len = in ? p.lengths[b] : 0;
+    const int n = in ? paged_chunks<D>(p, len) : 0;
+    const int incl = warp_scan(n, lane);
+    const unsigned hit = dec_ballot(run + incl > y);
+    if (hit != 0u) {
+      const int src = dec_lowest(hit);
+      PagedPlace r;
+      r.b = b0 + src;
+      r.n = dec_shfl(n, src);
+      r.len = dec_shfl(len, src);
+      const int before = run + dec_shfl(incl, src) - r.n;
+      const long long rem = x - static_cast<long long>(before) * HT;
+      r.ht = static_cast<int>(rem / r.n);
+      r.c = static_cast<int>(rem - static_cast<long long>(r.ht) * r.n);
+      if (r.ht >= HT) r.ht = HT - 1;
+      return r;
+    }
+    run += dec_shfl(incl, 31);
+  }
+  return PagedPlace{p.B, 0, 0, 1, 0};
+}
+
+// Grid: up to kPagedMaxCtas CTAs of kPagedThreads, paged_smem_bytes(D) of
+// dynamic shared memory.  UP: rows 8 .. 15 of the tile are used.
+template <int D, bool UP>
+__global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const PagedParams p) {
+  constexpr int CK = paged_chunk(D);  // keys per chunk
+  constexpr int PC = D / 8;           // 16-byte pieces per row
+  constexpr int NS = CK / 8;          // score n-tiles per chunk
+  constexpr int KS = D / 16;          // k-steps of q k^T
+  constexpr int NO = D / 8;           // output n-tiles
+  constexpr int TILE = CK * D * 2;    // bytes of K (of V) per chunk
+  constexpr int CB = 2 * TILE;
+  constexpr int NR = UP ? 2 : 1;      // fragment rows of a lane: g, g + 8
+  static_assert(TILE / 16 % 32 == 0 && CK % 16 == 0 && CK <= 32, "chunk");
+
+  dec_grid_dep_wait();
+  dec_grid_dep_launch();
+  uint8_t* smem = dec_dynamic_smem();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;  // fragment row, column pair
+  uint8_t* ring = smem + warp * (kPagedStages * CB);
+  int* slot_pos = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + warp * kPagedStages * 32;
+  int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + kPagedWarps * kPagedStages * 32;
+  int* totals = pre + kPagedThreads;
+  const int HT = p.Hkv * p.n_tiles;
+
+  // prefix sums of the requests' chunks, nb requests per thread
+  const int nb = (p.B + kPagedThreads - 1) / kPagedThreads;
+  int mine = 0;
+  for (int i = 0; i < nb; ++i) {
+    const int b = tid * nb + i;
+    if (b < p.B) mine += paged_chunks<D>(p, p.lengths[b]);
+  }
+  const int incl = warp_scan(mine, lane);
+  if (lane == 31) totals[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPagedWarps; ++w) {
+    if (w < warp) before += totals[w];
+    total += totals[w];
+  }
+  pre[tid] = before;
+  __syncthreads();
+
+  // this warp's run [s, e) of the flat axis
+  const long long W = static_cast<long long>(total) * HT;
+  long long nw = (W + kPagedMinRun - 1) / kPagedMinRun;
+  const long long n_warps = static_cast<long long>(gridDim.x) * kPagedWarps;
+  if (nw > n_warps) nw = n_warps;
+  const int gw = static_cast<int>(blockIdx.x) * kPagedWarps + warp;
+  if (gw >= nw) {
+    if (lane == 0) p.cuts[gw] = PagedCut{0, 0, 0, 0};
+    return;
+  }
+  const long long s = gw * W / nw, e = (gw + 1) * W / nw;
+  int left = static_cast<int>(e - s), to_issue = left;
+  PagedPlace use = paged_locate<D>(p, HT, nb, pre, s, lane), get = use;
+  bool begins = use.c == 0;  // the current item's first chunk is this warp's
+  PagedCut cut{0, 0, 0, 0};
+
+  // the page, the row in it and the position of lane's key of chunk `get`
+  int key_page, key_row, key_pos;
+  auto look_up = [&]() {
+    key_page = -1;
+    key_pos = kPagedNone;
+    key_row = 0;
+    const int vk = get.c * CK + lane;
+    const int li = vk / p.P;
+    const int row = vk - li * p.P;
+    int lp = -1;
+    if (lane < CK) {
+      if (p.pages != nullptr && get.b < p.B) {
+        const int h = get.ht / p.n_tiles;
+        const int have = paged_keys(p, get.len) / p.P;
+        if (li < have) lp = p.pages[(static_cast<long long>(get.b) * p.Hkv + h) * p.n_sel + li];
+      } else {
+        lp = li;
+      }
+    }
+    if (get.b < p.B && lp >= 0 && lp < p.width && lp * p.P + row < get.len) {
+      const int page = p.table[get.b * p.table_sb + lp];
+      if (page >= 0 && page < p.n_pages) {
+        key_page = page;
+        key_row = row;
+        key_pos = lp * p.P + row;
+      }
+    }
+  };
+  // chunk `get` into ring slot `slot`; rows of keys that are not held are
+  // zero-filled (and masked below)
+  auto issue = [&](int slot) {
+    uint8_t* sk = ring + slot * CB;
+    uint8_t* sv = sk + TILE;
+    const int h = get.ht / p.n_tiles;
+    const __nv_bfloat16* kb = p.k + h * p.k_sh;
+    const __nv_bfloat16* vb = p.v + h * p.v_sh;
+    slot_pos[slot * 32 + lane] = key_pos;
+#pragma unroll
+    for (int u = 0; u < TILE / 16 / 32; ++u) {
+      const int piece = lane + 32 * u, row = piece / PC, pc = piece - (piece / PC) * PC;
+      const int page = dec_shfl(key_page, row), in = dec_shfl(key_row, row);
+      const bool ok = page >= 0;
+      const long long pg = ok ? page : 0;
+      dec_cp_async16(sk + dec_swz<D>(row, pc), kb + pg * p.k_sp + in * p.k_st + pc * 8, ok);
+      dec_cp_async16(sv + dec_swz<D>(row, pc), vb + pg * p.v_sp + in * p.v_st + pc * 8, ok);
+    }
+  };
+
+  look_up();
+  // one commit group per ring slot, empty when the run is shorter
+#pragma unroll
+  for (int i = 0; i < kPagedStages; ++i) {
+    if (to_issue > 0) {
+      issue(i);
+      if (--to_issue > 0) {
+        paged_next<D>(p, HT, get);
+        look_up();
+      }
+    }
+    dec_cp_async_commit();
+  }
+
+  const float sl2 = p.scale_log2;
+  uint32_t qa[KS][4];          // query rows as mma A fragments
+  float o[NO][4];              // running state of rows g (and g + 8)
+  float m_run[NR], l_run[NR];  // (l is the lane's part)
+  int row_pos[NR];             // the rows' positions
+  bool fresh = true;
+  int slot = 0;
+
+  while (left > 0) {
+    const int h = use.ht / p.n_tiles, r0 = (use.ht - h * p.n_tiles) * kPagedRows;
+    if (fresh) {  // a new item: its query rows, zero past the last
+      fresh = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int gr = r0 + g + 8 * r;
+        const bool ok = r < NR && gr < p.rows && use.b < p.B;
+        const int gh = ok ? gr / p.Tq : 0, t = ok ? gr - gh * p.Tq : 0;
+        const __nv_bfloat16* qr =
+            p.q + use.b * p.q_sb + (static_cast<long long>(h) * (p.rows / p.Tq) + gh) * p.q_sh +
+            t * p.q_st;
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+          qa[kk][r] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 2 * t4) : 0u;
+          qa[kk][2 + r] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 8 + 2 * t4) : 0u;
+        }
+        if (r < NR) {
+          row_pos[r] = use.len - p.Tq + t;
+          m_run[r] = -INFINITY;
+          l_run[r] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    }
+    dec_cp_async_wait<kPagedStages - 1>();
+    __syncwarp();  // every lane's pieces of the chunk are in shared memory
+    const uint8_t* sk = ring + slot * CB;
+    uint8_t* sv = ring + slot * CB + TILE;
+    const int* pos = slot_pos + slot * 32;
+    const int pos0 = use.len - p.Tq;  // position of query t = 0
+
+    // s = q k^T: lane's c0, c1 are row g, keys 8 nt + 2 t4, + 1; c2, c3 row g + 8
+    float sc[NS][4];
+#pragma unroll
+    for (int nt = 0; nt < NS; ++nt) {
+      sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      if constexpr (PC >= 4) {
+#pragma unroll
+        for (int x = 0; x < PC / 4; ++x) {
+          uint32_t r[4];
+          dec_ldsm_x4(r, sk + dec_swz<D>(nt * 8 + (lane & 7), 4 * x + (lane >> 3)));
+          dec_mma(sc[nt], qa[2 * x][0], qa[2 * x][1], qa[2 * x][2], qa[2 * x][3], r[0], r[1]);
+          dec_mma(sc[nt], qa[2 * x + 1][0], qa[2 * x + 1][1], qa[2 * x + 1][2], qa[2 * x + 1][3],
+                  r[2], r[3]);
+        }
+      } else {  // D = 16: one k-step
+        uint32_t r[2];
+        dec_ldsm_x2(r, sk + dec_swz<D>(nt * 8 + (lane & 7), (lane >> 3) & 1));
+        dec_mma(sc[nt], qa[0][0], qa[0][1], qa[0][2], qa[0][3], r[0], r[1]);
+      }
+    }
+    // keys that are not held, and keys behind a row's position
+    const int my_pos = lane < CK ? pos[lane] : -1;
+    const bool masked = dec_ballot(my_pos > pos0) != 0u;
+    if (masked) {
+#pragma unroll
+      for (int nt = 0; nt < NS; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int kp = pos[nt * 8 + 2 * t4 + c];
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (kp > row_pos[r]) sc[nt][2 * r + c] = -INFINITY;
+        }
+    }
+
+    // online softmax of the rows over this chunk
+    float alpha[NR];
+    uint32_t hi[NS][NR], lo[NS][NR];  // the weights as bf16 pairs, hi + lo
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < NS; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][2 * r], sc[nt][2 * r + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float m_new = fmaxf(m_run[r], mx * sl2);
+      const float mu = m_new == -INFINITY ? 0.f : m_new;  // no visible key yet
+      alpha[r] = exp2f(m_run[r] - mu);                     // 0 while m_run is -inf
+      m_run[r] = m_new;
+      float ls = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NS; ++nt) {
+        const float p0 = exp2f(fmaf(sc[nt][2 * r], sl2, -mu));
+        const float p1 = exp2f(fmaf(sc[nt][2 * r + 1], sl2, -mu));
+        ls += p0 + p1;
+        sc[nt][2 * r] = p0;
+        sc[nt][2 * r + 1] = p1;
+        hi[nt][r] = dec_pack_bf16(p0, p1);
+        lo[nt][r] = dec_pack_bf16(p0 - dec_bf16_lo(hi[nt][r]), p1 - dec_bf16_hi(hi[nt][r]));
+      }
+      l_run[r] = fmaf(l_run[r], alpha[r], ls);
+    }
+#pragma unroll
+    for (int j = 0; j < NO; ++j) {
+      o[j][0] *= alpha[0];
+      o[j][1] *= alpha[0];
+      if constexpr (UP) {
+        o[j][2] *= alpha[1];
+        o[j][3] *= alpha[1];
+      }
+    }
+    // A key that some rows see and others do not: its value must not touch
+    // those others, not even as 0 * NaN.  Its products are done one by one,
+    // and its row of V is cleared for the matrix product below.
+    if (masked && p.Tq > 1) {
+      for (int key = 0; key < CK; ++key) {
+        const int kp = pos[key];
+        if (kp <= pos0 || kp == kPagedNone) continue;
+        const int nt = key >> 3, src = (lane & ~3) | ((key & 7) >> 1);
+        float w[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          float x = 0.f;
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+            if (n == nt) x = (key & 1) ? sc[n][2 * r + 1] : sc[n][2 * r];
+          w[r] = dec_shfl(x, src);
+        }
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+          const uint32_t vv =
+              *reinterpret_cast<const uint32_t*>(sv + dec_swz<D>(key, j) + 4 * t4);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (kp <= row_pos[r]) {
+              o[j][2 * r] = fmaf(w[r], dec_bf16_lo(vv), o[j][2 * r]);
+              o[j][2 * r + 1] = fmaf(w[r], dec_bf16_hi(vv), o[j][2 * r + 1]);
+            }
+        }
+        __syncwarp();  // every lane has read the row
+        if (lane < PC) *reinterpret_cast<uint4*>(sv + dec_swz<D>(key, lane)) = uint4{0, 0, 0, 0};
+      }
+      __syncwarp();  // the cleared rows are visible
+    }
+
+    // o += p v over the chunk's 16-key steps; one transposed x4 covers 16
+    // keys x 16 columns (two output n-tiles)
+#pragma unroll
+    for (int kk = 0; kk < CK / 16; ++kk) {
+#pragma unroll
+      for (int jj = 0; jj < D / 16; ++jj) {
+        const int mi = lane >> 3;
+        uint32_t r[4];
+        dec_ldsm_x4_t(r, sv + dec_swz<D>(kk * 16 + (mi & 1) * 8 + (lane & 7), 2 * jj + (mi >> 1)));
+        const uint32_t h1 = UP ? hi[2 * kk][NR - 1] : 0u, h3 = UP ? hi[2 * kk + 1][NR - 1] : 0u;
+        const uint32_t l1 = UP ? lo[2 * kk][NR - 1] : 0u, l3 = UP ? lo[2 * kk + 1][NR - 1] : 0u;
+        dec_mma(o[2 * jj], hi[2 * kk][0], h1, hi[2 * kk + 1][0], h3, r[0], r[1]);
+        dec_mma(o[2 * jj + 1], hi[2 * kk][0], h1, hi[2 * kk + 1][0], h3, r[2], r[3]);
+        dec_mma(o[2 * jj], lo[2 * kk][0], l1, lo[2 * kk + 1][0], l3, r[0], r[1]);
+        dec_mma(o[2 * jj + 1], lo[2 * kk][0], l1, lo[2 * kk + 1][0], l3, r[2], r[3]);
+      }
+    }
+    __syncwarp();  // every lane has read the slot: refill it
+    if (to_issue > 0) {
+      issue(slot);
+      if (--to_issue > 0) {
+        paged_next<D>(p, HT, get);
+        look_up();
+      }
+    }
+    dec_cp_async_commit();
+    slot = slot + 1 == kPagedStages ? 0 : slot + 1;
+    --left;
+
+    const bool ends = use.c + 1 == use.n;
+    if (ends || left == 0) {
+      const bool whole = ends && begins;
+      const int which = begins ? 1 : 0;
+      const long long part = (2LL * gw + which) * p.R;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float l = l_run[r];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int gr = r0 + g + 8 * r;
+        if (gr >= p.rows || use.b >= p.B) continue;
+        if (whole) {
+          const int gh = gr / p.Tq, t = gr - gh * p.Tq;
+          const long long hq = static_cast<long long>(h) * (p.rows / p.Tq) + gh;
+          __nv_bfloat16* ob = p.o + use.b * p.o_sb + hq * p.o_sh + t * p.o_st;
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+#pragma unroll
+          for (int j = 0; j < NO; ++j)
+            *reinterpret_cast<uint32_t*>(ob + 8 * j + 2 * t4) =
+                dec_pack_bf16(o[j][2 * r] * inv, o[j][2 * r + 1] * inv);
+          if (t4 == 0)
+            p.lse[(use.b * static_cast<long long>(p.H) + hq) * p.Tq + t] =
+                l == 0.f ? -INFINITY : (m_run[r] + log2f(l)) * 0.69314718055994531f;
+        } else {
+          const long long at = part + g + 8 * r;
+          if (t4 == 0) p.part_ml[at] = float2{m_run[r], l};
+#pragma unroll
+          for (int j = 0; j < NO; ++j)
+            *reinterpret_cast<float2*>(p.part_o + at * D + 8 * j + 2 * t4) =
+                float2{o[j][2 * r], o[j][2 * r + 1]};
+        }
+      }
+      if (begins && !ends) {  // cut here: the warps that hold its other chunks
+        const long long last = s + (e - s) - 1 + (use.n - 1 - use.c);  // its last flat chunk
+        long long w1 = ((last + 1) * nw - 1) / W;
+        if (w1 >= nw) w1 = nw - 1;
+        cut = PagedCut{use.b, use.ht, static_cast<int>(w1 - gw) + 1, 0};
+      }
+      begins = true;
+      fresh = true;
+    }
+    if (left > 0) paged_next<D>(p, HT, use);
+  }
+  dec_cp_async_wait<0>();
+  if (lane == 0) p.cuts[gw] = cut;
+}
+
+// Joins the parts of the cut items: CTA w that of the item that begins in
+// warp w of paged_decode_kernel, if one does.  A warp takes a row and every
+// n-th of its parts:  M = max m_i,  o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedParams p) {
+  constexpr int NW = kMergeThreads / 32;
+  constexpr int VEC = D >= 128 ? 4 : D >= 64 ? 2 : 1;  // columns of a lane
+  dec_grid_dep_wait();
+  dec_grid_dep_launch();
+  float* sh = reinterpret_cast<float*>(dec_dynamic_smem());  // [NW][2 + D]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gw = static_cast<int>(blockIdx.x);
+  const PagedCut cut = p.cuts[gw];
+  if (cut.n_parts == 0) return;
+  const int h = cut.ht / p.n_tiles, r0 = (cut.ht - h * p.n_tiles) * kPagedRows;
+  const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;
+  int team = NW;  // warps per row
+  while (team > 1 && team * rows > NW) team /= 2;
+  const int per = NW / team;  // rows at a time
+  for (int base = 0; base < rows; base += per) {
+    const int row = base + warp / team, k = warp % team;
+    float M = -INFINITY, L = 0.f, acc[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) acc[c] = 0.f;
+    if (row < rows) {
+      for (int i = k; i < cut.n_parts; i += team) {
+        const long long at = (2LL * (gw + i) + (i == 0 ? 1 : 0)) * p.R + row;
+        const float2 ml = p.part_ml[at];
+        if (ml.y == 0.f) continue;  // no key seen (a NaN goes on)
+        float v[VEC];
+        const float* src = p.part_o + at * D + lane * VEC;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) v[c] = lane * VEC < D ? src[c] : 0.f;
+        const float m_new = fmaxf(M, ml.x), mu = m_new == -INFINITY ? 0.f : m_new;
+        const float fa = exp2f(M - mu), fb = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mu);
+        M = m_new;
+        L = fmaf(L, fa, fb * ml.y);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[c] = fmaf(acc[c], fa, fb * v[c]);
+      }
+      float* mine = sh + warp * (2 + D);
+      if (lane == 0) {
+        mine[0] = M;
+        mine[1] = L;
+      }
+#pragma unroll
+      for (int c = 0; c < VEC; ++c)
+        if (lane * VEC < D) mine[2 + lane * VEC + c] = acc[c];
+    }
+    __syncthreads();
+    if (row < rows && k == 0) {
+      for (int j = 1; j < team; ++j) {
+        const float* other = sh + (warp + j) * (2 + D);
+        const float mj = other[0], lj = other[1];
+        if (lj == 0.f) continue;
+        const float m_new = fmaxf(M, mj), mu = m_new == -INFINITY ? 0.f : m_new;
+        const float fa = exp2f(M - mu), fb = mj == -INFINITY ? 1.f : exp2f(mj - mu);
+        M = m_new;
+        L = fmaf(L, fa, fb * lj);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+          if (lane * VEC < D) acc[c] = fmaf(acc[c], fa, fb * other[2 + lane * VEC + c]);
+      }
+      const int gr = r0 + row, gh = gr / p.Tq, t = gr - gh * p.Tq;
+      const long long hq = static_cast<long long>(h) * (p.rows / p.Tq) + gh;
+      __nv_bfloat16* ob = p.o + cut.b * p.o_sb + hq * p.o_sh + t * p.o_st;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int c = 0; c < VEC; ++c)
+        if (lane * VEC < D) ob[lane * VEC + c] = __float2bfloat16_rn(acc[c] * inv);
+      if (lane == 0)
+        p.lse[(cut.b * static_cast<long long>(p.H) + hq) * p.Tq + t] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    }
+    __syncthreads();
+  }
+}
+
+__host__ __device__ constexpr int paged_merge_smem_bytes(int D) {
+  return kMergeThreads / 32 * (2 + D) * 4;
+}
+
+}  // namespace cattn

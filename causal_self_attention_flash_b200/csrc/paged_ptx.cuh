@@ -1,0 +1,45 @@
+// Warp-level primitives of the paged-cache kernels, beside those of
+// decode_ptx.cuh.  The CPU emulator (tests/emu) defines the same functions
+// on the host, so that the kernels' sources run there unchanged.
+#pragma once
+
+#include <cstdint>
+
+#include "decode_ptx.cuh"
+
+namespace cattn {
+
+constexpr unsigned kFullWarp = 0xffffffffu;
+
+// The value of lane `src` (0..31) of the warp.
+__device__ __forceinline__ int dec_shfl(int v, int src) { return __shfl_sync(kFullWarp, v, src); }
+__device__ __forceinline__ float dec_shfl(float v, int src) {
+  return __shfl_sync(kFullWarp, v, src);
+}
+__device__ __forceinline__ long long dec_shfl(long long v, int src) {
+  return __shfl_sync(kFullWarp, v, src);
+}
+__device__ __forceinline__ double dec_shfl(double v, int src) {
+  return __shfl_sync(kFullWarp, v, src);
+}
+// The warp's predicate bits, lane l in bit l.
+__device__ __forceinline__ unsigned dec_ballot(bool p) { return __ballot_sync(kFullWarp, p); }
+__device__ __forceinline__ int dec_popc(unsigned x) { return __popc(x); }
+// Index of the lowest set bit (x != 0).
+__device__ __forceinline__ int dec_lowest(unsigned x) { return __ffs(static_cast<int>(x)) - 1; }
+// atomicAdd on a shared counter.
+__device__ __forceinline__ int dec_add_shared(int* p, int v) { return atomicAdd(p, v); }
+__device__ __forceinline__ long long dec_double_bits(double x) { return __double_as_longlong(x); }
+// Rank of the CTA in its cluster, and the cluster's size.
+__device__ __forceinline__ unsigned dec_cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+// bf16 halves of a word as floats (exact).
+__device__ __forceinline__ float dec_bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float dec_bf16_hi(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+
+}  // namespace cattn

@@ -316,6 +316,171 @@ CATTN_API cattn_status attn_decode(const void* q, cattn_layout lq, const void* k
                                    float* lse, void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* Paged key/value cache: decode attention for many sequences at once.
+ *
+ * generate() ("nanoGPT: a real GPT in two 300-line files", section 2) adds
+ * one token per step to one sequence; a server does so for many sequences of
+ * different lengths.  Their cached keys and values lie in pages of page_size
+ * positions in one pool, k_cache and v_cache, bf16 (n_pages, Hkv, page_size,
+ * D) with the layout { page, head, position } (cattn_layout's b, h, t; a
+ * (n_pages, page_size, Hkv, D) pool is { page_size*Hkv*D, D, Hkv*D }).
+ * block_table, int32 (B, width) with rows table_stride apart, holds the
+ * pages of each request: position p of request b is row p % page_size of
+ * page block_table[b][p / page_size].  An entry outside 0 .. n_pages - 1 is
+ * a page that is not held: nothing is read or written there, and its keys
+ * take no part in the attention.  Lengths, tables, slots and counts stay on
+ * the device, so a step can be captured in a CUDA graph and replayed as the
+ * requests grow.
+ *
+ * A step of a server is
+ *   attn_paged_plan      pages, slots and positions of the new tokens
+ *   per layer:
+ *     attn_cache_append  the new keys and values into their slots
+ *     attn_decode_paged  attention of the new positions, or
+ *     attn_page_select and attn_decode_sparse, over the best pages only.
+ *
+ * Limits common to these calls: D as above, H a multiple of Hkv (query head
+ * i reads cache head i / (H / Hkv)), width * page_size <= 2^30, page_size
+ * >= 1.  Layout rules as for the _strided calls.  Lengths below 0 count as
+ * 0. */
+
+/* Plan of a step: gives the new tokens their pages, slots and positions.
+ *
+ *   new_tokens  int32 (B): tokens that request b adds; 0: none; negative:
+ *               the request ends and its pages become free (its new length
+ *               is 0; its row of the table is left as it is)
+ *   lengths     int32 (B): positions that are cached
+ *   block_table int32 (B, width), in/out: entries of new pages are written
+ *   free_ring   int32 (n_pages), in/out, and ring_state int64 (2) = { head,
+ *               tail }, 0 <= head <= tail <= head + n_pages: the free pages
+ *               are free_ring[i % n_pages], head <= i < tail.  An empty cache
+ *               has 0 .. n_pages - 1 there and { 0, n_pages }.  New pages are
+ *               taken at the head in the order of the requests, freed ones
+ *               put at the tail (and given out by later calls only)
+ *   n_slots     capacity of slots and positions
+ *   lengths_out, ring_state_out  the values after the step; may be lengths
+ *               and ring_state themselves
+ *   cu_new      int32 (B + 1): first new token of each request, and their sum
+ *   slots       int64 (n_slots): page * page_size + row of each new token, in
+ *               the order of the requests (-1 where its page is not held),
+ *               then -1
+ *   positions   int32 (n_slots): its position, then -1
+ *   status      int32 (1): CATTN_OK; or CATTN_ERR_TOO_LARGE (too few free
+ *               pages, slots or table columns) or CATTN_ERR_INVALID_ARG (a
+ *               negative length, ring_state out of range, a request that
+ *               ends with more pages than its row holds), and then nothing
+ *               is changed: lengths_out = lengths, ring_state_out =
+ *               ring_state, cu_new = 0, slots = positions = -1
+ *
+ * Pages belong to one request.  Apart from the pairs named above no two
+ * arrays may overlap.  One launch.  Errors: CATTN_ERR_INVALID_ARG,
+ * CATTN_ERR_UNSUPPORTED (B above 8192, device), CATTN_ERR_CUDA. */
+CATTN_API cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
+                                       int32_t* block_table, long long table_stride,
+                                       int32_t* free_ring, const int64_t* ring_state, int B,
+                                       int width, int n_pages, int page_size, long long n_slots,
+                                       int32_t* lengths_out, int64_t* ring_state_out,
+                                       int32_t* cu_new, int64_t* slots, int32_t* positions,
+                                       int32_t* status, void* stream);
+
+/* Writes n new keys and values into the cache.
+ *
+ *   k_new, v_new  bf16 (n, Hkv, D), layouts lkn, lvn (t: from token to token,
+ *                 h: from head to head; b is not read): views of a fused
+ *                 projection as well as packed rows
+ *   slots         int64 (n), as attn_paged_plan writes them; one outside
+ *                 0 .. n_pages * page_size - 1 is skipped
+ *   bounds        bf16 (n_pages, Hkv, 2, D) contiguous, or NULL: the lowest
+ *                 and the highest value of each channel of a page's keys,
+ *                 kept for attn_page_select.  A run of tokens with ascending
+ *                 slots in a page joins its bounds; if it starts at the
+ *                 page's first row they start over.  NaN in, NaN out.
+ *
+ * Slots must differ from one another, and with bounds the tokens of a page
+ * must form one run of neighbours (as in the plan); otherwise the rows (the
+ * bounds) concerned are either token's.  The inputs must not overlap the
+ * cache.  Errors: CATTN_ERR_INVALID_ARG (a cache layout that overlaps itself
+ * included), CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  n = 0 is a no-op. */
+CATTN_API cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, const void* v_new,
+                                         cattn_layout lvn, long long n, int Hkv, int D,
+                                         int n_pages, int page_size, const int64_t* slots,
+                                         void* k_cache, cattn_layout lk, void* v_cache,
+                                         cattn_layout lv, void* bounds, void* stream);
+
+/* attn_decode over a paged cache: for every request b, the query rows at the
+ * positions lengths[b] - Tq .. lengths[b] - 1 (whose keys are in the cache)
+ * against the keys at or before them.
+ *
+ *   q    bf16 (B, H, Tq, D), layout lq, 1 <= Tq <= 8 (above:
+ *        CATTN_ERR_UNSUPPORTED)
+ *   o    bf16 (B, H, Tq, D) out, layout lo;  lse fp32 (B, H, Tq) out,
+ *        contiguous, natural log.  A row that sees no key (length 0, a
+ *        position below 0, no page held) has o = 0 and lse = -inf
+ *   workspace  device memory of attn_decode_paged_workspace_bytes bytes (0
+ *        for an empty or invalid shape), 256-byte aligned; no contents needed
+ *        on entry.  Calls that share one must not overlap on the GPU.
+ *
+ * Keys past a request's length are not read.  A key that a row does not see
+ * does not touch its result, whatever its values.  Two launches; results do
+ * not depend on the run.  Errors: CATTN_ERR_INVALID_ARG (as attn_decode;
+ * Hkv, page_size, width or table_stride out of range; a small or misaligned
+ * workspace), CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  B = 0 or H = 0 is a
+ * no-op. */
+CATTN_API size_t attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int Tq, int D);
+
+CATTN_API cattn_status attn_decode_paged(const void* q, cattn_layout lq, const void* k_cache,
+                                         cattn_layout lk, const void* v_cache, cattn_layout lv,
+                                         float scale, int B, int H, int Hkv, int Tq, int D,
+                                         int n_pages, int page_size, const int32_t* block_table,
+                                         long long table_stride, int width,
+                                         const int32_t* lengths, void* o, cattn_layout lo,
+                                         float* lse, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/* Pages that promise the largest scores.  For request b and cache head h,
+ * with q_r its (H / Hkv) Tq query rows and lo, hi the bounds of page i of the
+ * request,
+ *
+ *   s_i = max_r sum_d max(q_rd, 0) hi_d + min(q_rd, 0) lo_d
+ *
+ * bounds every q_r . k in the page from above.  Of the request's
+ * n = min(ceil(lengths[b] / page_size), width) pages the n_first first and
+ * n_last last are taken, then those of the highest s_i (the lower index
+ * where equal; a page that is not held last, a NaN first) up to n_select, or
+ * all n if there are no more.  The scores are compared as exact sums.
+ *
+ *   bounds  bf16 (n_pages, Hkv, 2, D) contiguous (attn_cache_append)
+ *   pages   int32 (B, Hkv, n_select) out: indices into the request's row of
+ *           the table, ascending, then -1
+ *   workspace  as for attn_decode_paged, of
+ *           attn_page_select_workspace_bytes(B, Hkv, width) bytes; may be
+ *           NULL where width <= n_select
+ *
+ * Errors: CATTN_ERR_INVALID_ARG (n_select < 1, n_first or n_last < 0,
+ * n_first + n_last > n_select, ...), CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA. */
+CATTN_API size_t attn_page_select_workspace_bytes(int B, int Hkv, int width);
+
+CATTN_API cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds, int B,
+                                        int H, int Hkv, int Tq, int D, int n_pages, int page_size,
+                                        const int32_t* block_table, long long table_stride,
+                                        int width, const int32_t* lengths, int n_select,
+                                        int n_first, int n_last, int32_t* pages, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* attn_decode_paged over listed pages only: pages int32 (B, Hkv, n_select)
+ * contiguous, as attn_page_select writes them.  Of a request with n pages the
+ * first min(n_select, n) entries of each list are read; one outside
+ * 0 .. width - 1 lists nothing, and a page that is listed twice counts
+ * twice.  Everything else as attn_decode_paged (its workspace too). */
+CATTN_API cattn_status attn_decode_sparse(const void* q, cattn_layout lq, const void* k_cache,
+                                          cattn_layout lk, const void* v_cache, cattn_layout lv,
+                                          float scale, int B, int H, int Hkv, int Tq, int D,
+                                          int n_pages, int page_size, const int32_t* block_table,
+                                          long long table_stride, int width,
+                                          const int32_t* lengths, const int32_t* pages,
+                                          int n_select, void* o, cattn_layout lo, float* lse,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Backward pass for callers that cannot allocate device memory.
  *
  * Same computation, arguments and results as attn_bwd, minus the workspace:
@@ -403,7 +568,9 @@ CATTN_API cattn_status cattn_selftest_wait_timeout_ws(uint32_t timeout_us, void*
  * launching stream.  cattn_timing_read() waits for the recorded events and
  * returns, per kernel, the summed device time in ms and the launch count,
  * then forgets them.  Kernel index: 0 forward, 1 backward preprocess,
- * 2 backward main, 3 dQ convert, 4 decode (its two kernels together).
+ * 2 backward main, 3 dQ convert, 4 decode (attn_decode, or the two kernels
+ * of attn_decode_paged and _sparse together), 5 attn_paged_plan and
+ * attn_cache_append, 6 attn_page_select (its two kernels together).
  * n = length of both output arrays (indices >= n are dropped).  Not
  * for use while a stream is being captured into a CUDA graph. */
 CATTN_API void cattn_timing_enable(int enable);

@@ -1,0 +1,70 @@
+// Host definitions of the paged-cache kernels' warp primitives (the functions
+// of paged_ptx.cuh), for the CPU emulator: indexed shuffles, ballots, the
+// cluster rank, counters in shared memory, bit casts.
+#pragma once
+
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <stdexcept>
+
+#include "decode_ptx_emu.h"
+
+struct alignas(8) int2 {
+  int x, y;
+};
+
+namespace cattn {
+
+constexpr unsigned kFullWarp = 0xffffffffu;
+
+namespace emu_detail {
+template <typename T>
+inline T shfl(T v, int src) {
+  if (src < 0 || src > 31) throw std::logic_error("shuffle from a lane outside the warp");
+  uint64_t mine = 0;
+  std::memcpy(&mine, &v, sizeof(T));
+  const uint64_t* all = emu::warp_exchange(&mine, 1);
+  T r;
+  std::memcpy(&r, all + src * emu::kWords, sizeof(T));
+  return r;
+}
+}  // namespace emu_detail
+
+inline int dec_shfl(int v, int src) { return emu_detail::shfl(v, src); }
+inline float dec_shfl(float v, int src) { return emu_detail::shfl(v, src); }
+inline long long dec_shfl(long long v, int src) { return emu_detail::shfl(v, src); }
+inline double dec_shfl(double v, int src) { return emu_detail::shfl(v, src); }
+inline unsigned dec_ballot(bool p) {
+  const uint64_t mine = p;
+  const uint64_t* all = emu::warp_exchange(&mine, 1);
+  unsigned r = 0;
+  for (int l = 0; l < 32; ++l) r |= (all[l * emu::kWords] ? 1u : 0u) << l;
+  return r;
+}
+inline int dec_popc(unsigned x) { return __builtin_popcount(x); }
+inline int dec_lowest(unsigned x) { return __builtin_ctz(x); }
+inline int dec_add_shared(int* p, int v) {
+  emu::check_smem(p, 4, 4);
+  return std::atomic_ref<int>(*p).fetch_add(v);
+}
+inline long long dec_double_bits(double x) {
+  long long r;
+  std::memcpy(&r, &x, 8);
+  return r;
+}
+inline unsigned dec_cluster_rank() { return emu::t_cta->rank; }
+inline float dec_bf16_lo(uint32_t w) {
+  const uint32_t u = w << 16;
+  float f;
+  std::memcpy(&f, &u, 4);
+  return f;
+}
+inline float dec_bf16_hi(uint32_t w) {
+  const uint32_t u = w & 0xffff0000u;
+  float f;
+  std::memcpy(&f, &u, 4);
+  return f;
+}
+
+}  // namespace cattn
