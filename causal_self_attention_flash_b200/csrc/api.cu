@@ -749,8 +749,9 @@ cattn_status paged_impl(const PagedParams& p, int grid, int dev, cudaStream_t s)
   cudaError_t e = launch_dependent(true, paged_decode_kernel<D, UP>, dim3(grid),
                                    dim3(kPagedThreads), paged_smem_bytes(D), s, p);
   if (e == cudaSuccess)
-    e = launch_dependent(true, paged_merge_kernel<D>, dim3(grid * kPagedWarps),
-                         dim3(kMergeThreads), paged_merge_smem_bytes(D), s, p);
+    e = launch_dependent(true, paged_merge_kernel<D>, dim3(grid * paged_merge_y(p.R)),
+                         dim3(kMergeThreads), paged_merge_smem_bytes(D), s, p,
+                         paged_merge_y(p.R));
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 

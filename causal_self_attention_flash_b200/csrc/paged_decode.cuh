@@ -137,6 +137,11 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, int HT, PagedPl
   x.n = paged_chunks<D>(p, x.len);
 }
 
+// Natural log-sum-exp from a base-2 maximum and sum.
+__device__ __forceinline__ float paged_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // Inclusive sum over the warp's lanes.
 __device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
@@ -184,100 +189,82 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
   return PagedPlace{p.B, 0, 0, 1, 0};
 }
 
-// Grid: up to kPagedMaxCtas CTAs of kPagedThreads, paged_smem_bytes(D) of
-// dynamic shared memory.  UP: rows 8 .. 15 of the tile are used.
+// One warp's work on chunks: its ring of shared memory slots and the running
+// state of the item it is in.  UP: rows 8 .. 15 of the tile are used.
 template <int D, bool UP>
-__global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const PagedParams p) {
-  constexpr int CK = paged_chunk(D);  // keys per chunk
-  constexpr int PC = D / 8;           // 16-byte pieces per row
-  constexpr int NS = CK / 8;          // score n-tiles per chunk
-  constexpr int KS = D / 16;          // k-steps of q k^T
-  constexpr int NO = D / 8;           // output n-tiles
-  constexpr int TILE = CK * D * 2;    // bytes of K (of V) per chunk
-  constexpr int CB = 2 * TILE;
-  constexpr int NR = UP ? 2 : 1;      // fragment rows of a lane: g, g + 8
+struct PagedWarp {
+  static constexpr int CK = paged_chunk(D);  // keys per chunk
+  static constexpr int PC = D / 8;           // 16-byte pieces per row
+  static constexpr int NS = CK / 8;          // score n-tiles per chunk
+  static constexpr int KS = D / 16;          // k-steps of q k^T
+  static constexpr int NO = D / 8;           // output n-tiles
+  static constexpr int TILE = CK * D * 2;    // bytes of K (of V) per chunk
+  static constexpr int CB = 2 * TILE;
+  static constexpr int NR = UP ? 2 : 1;      // fragment rows of a lane: g, g + 8
   static_assert(TILE / 16 % 32 == 0 && CK % 16 == 0 && CK <= 32, "chunk");
 
-  dec_grid_dep_wait();
-  dec_grid_dep_launch();
-  uint8_t* smem = dec_dynamic_smem();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t4 = lane & 3;  // fragment row, column pair
-  uint8_t* ring = smem + warp * (kPagedStages * CB);
-  int* slot_pos = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + warp * kPagedStages * 32;
-  int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + kPagedWarps * kPagedStages * 32;
-  int* totals = pre + kPagedThreads;
-  const int HT = p.Hkv * p.n_tiles;
+  const PagedParams& p;
+  int lane, g, t4;             // lane, fragment row, column pair
+  uint8_t* ring;
+  int* slot_pos;               // positions of the slots' keys
+  uint32_t qa[KS][4];          // query rows as mma A fragments
+  float o[NO][4];              // running state of rows g (and g + 8)
+  float m_run[NR], l_run[NR];  // (l is the lane's part)
+  int row_pos[NR];             // the rows' positions
+  int key_page, key_row, key_pos;  // looked up: the lane's key of the next chunk
 
-  // prefix sums of the requests' chunks, nb requests per thread
-  const int nb = (p.B + kPagedThreads - 1) / kPagedThreads;
-  int mine = 0;
-  for (int i = 0; i < nb; ++i) {
-    const int b = tid * nb + i;
-    if (b < p.B) mine += paged_chunks<D>(p, p.lengths[b]);
+  __device__ __forceinline__ PagedWarp(const PagedParams& params, uint8_t* smem, int warp,
+                                       int lane_)
+      : p(params), lane(lane_), g(lane_ >> 2), t4(lane_ & 3) {
+    ring = smem + warp * (kPagedStages * CB);
+    slot_pos = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + warp * kPagedStages * 32;
+    clear();
   }
-  const int incl = warp_scan(mine, lane);
-  if (lane == 31) totals[warp] = incl;
-  __syncthreads();
-  int before = incl - mine, total = 0;
+
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int w = 0; w < kPagedWarps; ++w) {
-    if (w < warp) before += totals[w];
-    total += totals[w];
+    for (int r = 0; r < NR; ++r) {
+      m_run[r] = -INFINITY;
+      l_run[r] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   }
-  pre[tid] = before;
-  __syncthreads();
 
-  // this warp's run [s, e) of the flat axis
-  const long long W = static_cast<long long>(total) * HT;
-  long long nw = (W + kPagedMinRun - 1) / kPagedMinRun;
-  const long long n_warps = static_cast<long long>(gridDim.x) * kPagedWarps;
-  if (nw > n_warps) nw = n_warps;
-  const int gw = static_cast<int>(blockIdx.x) * kPagedWarps + warp;
-  if (gw >= nw) {
-    if (lane == 0) p.cuts[gw] = PagedCut{0, 0, 0, 0};
-    return;
-  }
-  const long long s = gw * W / nw, e = (gw + 1) * W / nw;
-  int left = static_cast<int>(e - s), to_issue = left;
-  PagedPlace use = paged_locate<D>(p, HT, nb, pre, s, lane), get = use;
-  bool begins = use.c == 0;  // the current item's first chunk is this warp's
-  PagedCut cut{0, 0, 0, 0};
-
-  // the page, the row in it and the position of lane's key of chunk `get`
-  int key_page, key_row, key_pos;
-  auto look_up = [&]() {
+  // The page, the row in it and the position of the lane's key of chunk x.
+  __device__ __forceinline__ void look_up(const PagedPlace& x) {
     key_page = -1;
     key_pos = kPagedNone;
     key_row = 0;
-    const int vk = get.c * CK + lane;
+    const int vk = x.c * CK + lane;
     const int li = vk / p.P;
     const int row = vk - li * p.P;
     int lp = -1;
-    if (lane < CK) {
-      if (p.pages != nullptr && get.b < p.B) {
-        const int h = get.ht / p.n_tiles;
-        const int have = paged_keys(p, get.len) / p.P;
-        if (li < have) lp = p.pages[(static_cast<long long>(get.b) * p.Hkv + h) * p.n_sel + li];
+    if (lane < CK && x.b < p.B) {
+      if (p.pages != nullptr) {
+        const int h = x.ht / p.n_tiles;
+        const int have = paged_keys(p, x.len) / p.P;
+        if (li < have) lp = p.pages[(static_cast<long long>(x.b) * p.Hkv + h) * p.n_sel + li];
       } else {
         lp = li;
       }
     }
-    if (get.b < p.B && lp >= 0 && lp < p.width && lp * p.P + row < get.len) {
-      const int page = p.table[get.b * p.table_sb + lp];
+    if (lp >= 0 && lp < p.width && lp * p.P + row < x.len) {
+      const int page = p.table[x.b * p.table_sb + lp];
       if (page >= 0 && page < p.n_pages) {
         key_page = page;
         key_row = row;
         key_pos = lp * p.P + row;
       }
     }
-  };
-  // chunk `get` into ring slot `slot`; rows of keys that are not held are
-  // zero-filled (and masked below)
-  auto issue = [&](int slot) {
+  }
+
+  // Chunk x (looked up) into ring slot `slot`; rows of keys that are not
+  // held are zero-filled (and masked in chunk()).
+  __device__ __forceinline__ void issue(const PagedPlace& x, int slot) {
     uint8_t* sk = ring + slot * CB;
     uint8_t* sv = sk + TILE;
-    const int h = get.ht / p.n_tiles;
+    const int h = x.ht / p.n_tiles;
     const __nv_bfloat16* kb = p.k + h * p.k_sh;
     const __nv_bfloat16* vb = p.v + h * p.v_sh;
     slot_pos[slot * 32 + lane] = key_pos;
@@ -290,62 +277,42 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
       dec_cp_async16(sk + dec_swz<D>(row, pc), kb + pg * p.k_sp + in * p.k_st + pc * 8, ok);
       dec_cp_async16(sv + dec_swz<D>(row, pc), vb + pg * p.v_sp + in * p.v_st + pc * 8, ok);
     }
-  };
-
-  look_up();
-  // one commit group per ring slot, empty when the run is shorter
-#pragma unroll
-  for (int i = 0; i < kPagedStages; ++i) {
-    if (to_issue > 0) {
-      issue(i);
-      if (--to_issue > 0) {
-        paged_next<D>(p, HT, get);
-        look_up();
-      }
-    }
-    dec_cp_async_commit();
   }
 
-  const float sl2 = p.scale_log2;
-  uint32_t qa[KS][4];          // query rows as mma A fragments
-  float o[NO][4];              // running state of rows g (and g + 8)
-  float m_run[NR], l_run[NR];  // (l is the lane's part)
-  int row_pos[NR];             // the rows' positions
-  bool fresh = true;
-  int slot = 0;
+  // Query row `gr` of cache head h: its head and new position.
+  __device__ __forceinline__ long long row_head(int h, int gr, int* t) const {
+    const int gh = gr / p.Tq;
+    *t = gr - gh * p.Tq;
+    return static_cast<long long>(h) * (p.rows / p.Tq) + gh;
+  }
 
-  while (left > 0) {
-    const int h = use.ht / p.n_tiles, r0 = (use.ht - h * p.n_tiles) * kPagedRows;
-    if (fresh) {  // a new item: its query rows, zero past the last
-      fresh = false;
+  // A new item: its query rows (zero past the last) and an empty state.
+  __device__ __forceinline__ void begin(const PagedPlace& x) {
+    clear();
+    const int h = x.ht / p.n_tiles, r0 = (x.ht - h * p.n_tiles) * kPagedRows;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int gr = r0 + g + 8 * r;
-        const bool ok = r < NR && gr < p.rows && use.b < p.B;
-        const int gh = ok ? gr / p.Tq : 0, t = ok ? gr - gh * p.Tq : 0;
-        const __nv_bfloat16* qr =
-            p.q + use.b * p.q_sb + (static_cast<long long>(h) * (p.rows / p.Tq) + gh) * p.q_sh +
-            t * p.q_st;
+    for (int r = 0; r < 2; ++r) {
+      const int gr = r0 + g + 8 * r;
+      const bool ok = r < NR && gr < p.rows && x.b < p.B;
+      int t = 0;
+      const long long hq = ok ? row_head(h, gr, &t) : 0;
+      const __nv_bfloat16* qr = p.q + (ok ? x.b : 0) * p.q_sb + hq * p.q_sh + t * p.q_st;
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-          qa[kk][r] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 2 * t4) : 0u;
-          qa[kk][2 + r] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 8 + 2 * t4) : 0u;
-        }
-        if (r < NR) {
-          row_pos[r] = use.len - p.Tq + t;
-          m_run[r] = -INFINITY;
-          l_run[r] = 0.f;
-        }
+      for (int kk = 0; kk < KS; ++kk) {
+        qa[kk][r] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 2 * t4) : 0u;
+        qa[kk][2 + r] = ok ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 8 + 2 * t4) : 0u;
       }
-#pragma unroll
-      for (int j = 0; j < NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      if (r < NR) row_pos[r] = x.len - p.Tq + t;
     }
-    dec_cp_async_wait<kPagedStages - 1>();
-    __syncwarp();  // every lane's pieces of the chunk are in shared memory
+  }
+
+  // The chunk in ring slot `slot` of a request of length len.
+  __device__ __forceinline__ void chunk(int slot, int len) {
+    const float sl2 = p.scale_log2;
     const uint8_t* sk = ring + slot * CB;
     uint8_t* sv = ring + slot * CB + TILE;
     const int* pos = slot_pos + slot * 32;
-    const int pos0 = use.len - p.Tq;  // position of query t = 0
+    const int pos0 = len - p.Tq;  // position of query t = 0
 
     // s = q k^T: lane's c0, c1 are row g, keys 8 nt + 2 t4, + 1; c2, c3 row g + 8
     float sc[NS][4];
@@ -469,146 +436,368 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
         dec_mma(o[2 * jj + 1], lo[2 * kk][0], l1, lo[2 * kk + 1][0], l3, r[2], r[3]);
       }
     }
-    __syncwarp();  // every lane has read the slot: refill it
-    if (to_issue > 0) {
-      issue(slot);
-      if (--to_issue > 0) {
-        paged_next<D>(p, HT, get);
-        look_up();
-      }
+  }
+
+  // Row r's sum over the quad that shares it.
+  __device__ __forceinline__ float row_sum(int r) const {
+    float l = l_run[r];
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    return l + __shfl_xor_sync(0xffffffffu, l, 2);
+  }
+
+  // The item x, done: its rows' o and lse.
+  __device__ __forceinline__ void finish(const PagedPlace& x) {
+    const int h = x.ht / p.n_tiles, r0 = (x.ht - h * p.n_tiles) * kPagedRows;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float l = row_sum(r);
+      const int gr = r0 + g + 8 * r;
+      if (gr >= p.rows || x.b >= p.B) continue;
+      int t;
+      const long long hq = row_head(h, gr, &t);
+      __nv_bfloat16* ob = p.o + x.b * p.o_sb + hq * p.o_sh + t * p.o_st;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+        *reinterpret_cast<uint32_t*>(ob + 8 * j + 2 * t4) =
+            dec_pack_bf16(o[j][2 * r] * inv, o[j][2 * r + 1] * inv);
+      if (t4 == 0)
+        p.lse[(x.b * static_cast<long long>(p.H) + hq) * p.Tq + t] = paged_lse(m_run[r], l);
     }
+  }
+
+  // The state as rows [r] of ml (m, l) and of ov (o), R of them.
+  __device__ __forceinline__ void store(float2* ml, float* ov, int R) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float l = row_sum(r);
+      const int row = g + 8 * r;
+      if (row >= R) continue;
+      if (t4 == 0) ml[row] = float2{m_run[r], l};
+#pragma unroll
+      for (int j = 0; j < NO; ++j)
+        *reinterpret_cast<float2*>(ov + row * D + 8 * j + 2 * t4) =
+            float2{o[j][2 * r], o[j][2 * r + 1]};
+    }
+  }
+};
+
+// Shared memory of a CTA's merge, over the rings: (m, l) and o of each warp,
+// then the CTA's own.
+struct PagedMerge {
+  float2 *ml, *cta_ml;
+  float *ov, *cta_ov;
+};
+template <int D>
+__device__ __forceinline__ PagedMerge paged_merge_area(uint8_t* smem) {
+  static_assert((kPagedWarps + 1) * kPagedRows * (D + 2) * 4 <= paged_ring_bytes(D), "merge area");
+  PagedMerge a;
+  a.ml = reinterpret_cast<float2*>(smem);
+  a.cta_ml = a.ml + kPagedWarps * kPagedRows;
+  a.ov = reinterpret_cast<float*>(a.cta_ml + kPagedRows);
+  a.cta_ov = a.ov + kPagedWarps * kPagedRows * D;
+  return a;
+}
+
+// One more part (m, l) for a running (M, L): the factors of the two.  A part
+// without keys has l = 0; l = NaN goes on whatever its m.
+__device__ __forceinline__ void paged_join(float m, float l, float& M, float& L, float& fa,
+                                           float& fb) {
+  const float m_new = fmaxf(M, m), mu = m_new == -INFINITY ? 0.f : m_new;
+  fa = exp2f(M - mu);
+  fb = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - mu);
+  M = m_new;
+  L = fmaf(L, fa, fb * l);
+}
+
+// Grid: up to kPagedMaxCtas CTAs of kPagedThreads, paged_smem_bytes(D) of
+// dynamic shared memory.
+//
+// A CTA takes an even share of the flat axis.  If all of it lies in one item
+// the warps take turns at its chunks and join their results in shared
+// memory; otherwise each takes a quarter of the share.
+template <int D, bool UP>
+__global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const PagedParams p) {
+  dec_grid_dep_wait();
+  dec_grid_dep_launch();
+  uint8_t* smem = dec_dynamic_smem();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + kPagedWarps * kPagedStages * 32;
+  int* totals = pre + kPagedThreads;
+  const int HT = p.Hkv * p.n_tiles;
+
+  // prefix sums of the requests' chunks, nb requests per thread
+  const int nb = (p.B + kPagedThreads - 1) / kPagedThreads;
+  int mine = 0;
+  for (int i = 0; i < nb; ++i) {
+    const int b = tid * nb + i;
+    if (b < p.B) mine += paged_chunks<D>(p, p.lengths[b]);
+  }
+  const int incl = warp_scan(mine, lane);
+  if (lane == 31) totals[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPagedWarps; ++w) {
+    if (w < warp) before += totals[w];
+    total += totals[w];
+  }
+  pre[tid] = before;
+  __syncthreads();
+
+  // this CTA's share [S, E) of the flat axis
+  const long long W = static_cast<long long>(total) * HT;
+  long long nc = (W + kPagedMinRun * kPagedWarps - 1) / (kPagedMinRun * kPagedWarps);
+  if (nc > gridDim.x) nc = gridDim.x;
+  const int cta = static_cast<int>(blockIdx.x), gw = cta * kPagedWarps + warp;
+  if (cta >= nc) {
+    if (lane == 0) p.cuts[gw] = PagedCut{0, 0, 0, 0};
+    return;
+  }
+  const long long S = cta * W / nc, E = (cta + 1) * W / nc;
+  const int share = static_cast<int>(E - S);
+  PagedPlace use = paged_locate<D>(p, HT, nb, pre, S, lane);
+  const bool together = use.c + share <= use.n;  // one item's
+  const PagedPlace first = use;
+  const int step = together ? kPagedWarps : 1;
+  long long s = S + warp;
+  int left = share > warp ? (share - warp + kPagedWarps - 1) / kPagedWarps : 0;
+  if (together) {
+    use.c += warp;
+  } else {
+    s = S + static_cast<long long>(warp) * share / kPagedWarps;
+    left = static_cast<int>(S + static_cast<long long>(warp + 1) * share / kPagedWarps - s);
+    if (left > 0) use = paged_locate<D>(p, HT, nb, pre, s, lane);
+  }
+  // the warp that holds flat chunk x (at or behind S), and so the parts of an
+  // item that begins in this warp and ends with chunk x
+  auto parts_to = [&](long long x) {
+    if (x >= W) x = W - 1;
+    const long long c = ((x + 1) * nc - 1) / W, cs = c * W / nc, ce = (c + 1) * W / nc;
+    const long long w = ((x - cs + 1) * kPagedWarps - 1) / (ce - cs);
+    return static_cast<int>(c * kPagedWarps + w - gw) + 1;
+  };
+
+  PagedWarp<D, UP> k(p, smem, warp, lane);
+  PagedPlace get = use;
+  int to_issue = left;
+  auto issue = [&](int slot) {  // the next chunk, and the look-up of the one behind it
+    k.issue(get, slot);
+    if (--to_issue > 0) {
+      if (together) get.c += step; else paged_next<D>(p, HT, get);
+      k.look_up(get);
+    }
+  };
+  if (to_issue > 0) k.look_up(get);
+  // one commit group per ring slot, empty when the run is shorter
+#pragma unroll
+  for (int i = 0; i < kPagedStages; ++i) {
+    if (to_issue > 0) issue(i);
+    dec_cp_async_commit();
+  }
+
+  bool begins = use.c == 0;  // the current item's first chunk is this warp's
+  bool fresh = true;
+  PagedCut cut{0, 0, 0, 0};
+  int slot = 0;
+  while (left > 0) {
+    if (fresh) {
+      fresh = false;
+      k.begin(use);
+    }
+    dec_cp_async_wait<kPagedStages - 1>();
+    __syncwarp();  // every lane's pieces of the chunk are in shared memory
+    k.chunk(slot, use.len);
+    __syncwarp();  // every lane has read the slot: refill it
+    if (to_issue > 0) issue(slot);
     dec_cp_async_commit();
     slot = slot + 1 == kPagedStages ? 0 : slot + 1;
     --left;
-
+    if (together) {
+      use.c += step;
+      continue;
+    }
     const bool ends = use.c + 1 == use.n;
     if (ends || left == 0) {
-      const bool whole = ends && begins;
-      const int which = begins ? 1 : 0;
-      const long long part = (2LL * gw + which) * p.R;
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float l = l_run[r];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int gr = r0 + g + 8 * r;
-        if (gr >= p.rows || use.b >= p.B) continue;
-        if (whole) {
-          const int gh = gr / p.Tq, t = gr - gh * p.Tq;
-          const long long hq = static_cast<long long>(h) * (p.rows / p.Tq) + gh;
-          __nv_bfloat16* ob = p.o + use.b * p.o_sb + hq * p.o_sh + t * p.o_st;
-          const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
-#pragma unroll
-          for (int j = 0; j < NO; ++j)
-            *reinterpret_cast<uint32_t*>(ob + 8 * j + 2 * t4) =
-                dec_pack_bf16(o[j][2 * r] * inv, o[j][2 * r + 1] * inv);
-          if (t4 == 0)
-            p.lse[(use.b * static_cast<long long>(p.H) + hq) * p.Tq + t] =
-                l == 0.f ? -INFINITY : (m_run[r] + log2f(l)) * 0.69314718055994531f;
-        } else {
-          const long long at = part + g + 8 * r;
-          if (t4 == 0) p.part_ml[at] = float2{m_run[r], l};
-#pragma unroll
-          for (int j = 0; j < NO; ++j)
-            *reinterpret_cast<float2*>(p.part_o + at * D + 8 * j + 2 * t4) =
-                float2{o[j][2 * r], o[j][2 * r + 1]};
-        }
+      if (ends && begins) {
+        k.finish(use);
+      } else {
+        const long long part = (2LL * gw + begins) * p.R;
+        k.store(p.part_ml + part, p.part_o + part * D, p.R);
       }
-      if (begins && !ends) {  // cut here: the warps that hold its other chunks
-        const long long last = s + (e - s) - 1 + (use.n - 1 - use.c);  // its last flat chunk
-        long long w1 = ((last + 1) * nw - 1) / W;
-        if (w1 >= nw) w1 = nw - 1;
-        cut = PagedCut{use.b, use.ht, static_cast<int>(w1 - gw) + 1, 0};
-      }
+      if (begins && !ends)  // cut here: the warps that hold its other chunks
+        cut = PagedCut{use.b, use.ht,
+                       parts_to(S + static_cast<long long>(warp + 1) * share / kPagedWarps - 1 +
+                                (use.n - 1 - use.c)),
+                       0};
       begins = true;
       fresh = true;
     }
     if (left > 0) paged_next<D>(p, HT, use);
   }
   dec_cp_async_wait<0>();
+
+  if (together) {
+    const bool whole = first.c == 0 && share == first.n;
+    const PagedMerge a = paged_merge_area<D>(smem);
+    __syncthreads();  // every warp is done with its ring
+    k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, kPagedRows);
+    __syncthreads();
+    const int h = first.ht / p.n_tiles, r0 = (first.ht - h * p.n_tiles) * kPagedRows;
+    const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;
+    const long long part = (2LL * cta * kPagedWarps + (first.c == 0)) * p.R;
+    for (int i = tid; i < rows * D && first.b < p.B; i += kPagedThreads) {
+      const int r = i / D, d = i - r * D;
+      float M = -INFINITY, L = 0.f, acc = 0.f, fa, fb;
+#pragma unroll
+      for (int w = 0; w < kPagedWarps; ++w) {
+        const float2 ml = a.ml[w * kPagedRows + r];
+        paged_join(ml.x, ml.y, M, L, fa, fb);
+        acc = fmaf(acc, fa, fb * a.ov[(w * kPagedRows + r) * D + d]);
+      }
+      if (whole) {
+        int t;
+        const long long hq = k.row_head(h, r0 + r, &t);
+        p.o[first.b * p.o_sb + hq * p.o_sh + t * p.o_st + d] =
+            __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+        if (d == 0)
+          p.lse[(first.b * static_cast<long long>(p.H) + hq) * p.Tq + t] = paged_lse(M, L);
+      } else {
+        p.part_o[(part + r) * D + d] = acc;
+        if (d == 0) p.part_ml[part + r] = float2{M, L};
+      }
+    }
+    if (warp == 0 && first.c == 0 && !whole)
+      cut = PagedCut{first.b, first.ht, parts_to(S + first.n - 1), 0};
+  }
+  // nothing in slot 0 of a warp whose chunks are in the CTA's part, or that has none
+  if (together ? warp > 0 : E == S || s == S + static_cast<long long>(warp + 1) * share / kPagedWarps)
+    if (lane < p.R) p.part_ml[2LL * gw * p.R + lane] = float2{-INFINITY, 0.f};
   if (lane == 0) p.cuts[gw] = cut;
 }
 
-// Joins the parts of the cut items: CTA w that of the item that begins in
-// warp w of paged_decode_kernel, if one does.  A warp takes a row and every
-// n-th of its parts:  M = max m_i,  o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// Joins the parts of the cut items:  M = max m_i,
+//   o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// Grid: (CTAs of paged_decode_kernel) * n_y; CTA (c, y) takes rows y, y + n_y,
+// ... of the items that begin in CTA c's warps.  A team of warps takes a row
+// of an item, 32 parts at a time: the lanes read the parts' (m, l) at once,
+// then the warp adds up the o of those that hold keys.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedParams p, int n_y) {
   constexpr int NW = kMergeThreads / 32;
   constexpr int VEC = D >= 128 ? 4 : D >= 64 ? 2 : 1;  // columns of a lane
+  constexpr int ILP = 4;                               // parts in flight
   dec_grid_dep_wait();
   dec_grid_dep_launch();
   float* sh = reinterpret_cast<float*>(dec_dynamic_smem());  // [NW][2 + D]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gw = static_cast<int>(blockIdx.x);
-  const PagedCut cut = p.cuts[gw];
-  if (cut.n_parts == 0) return;
-  const int h = cut.ht / p.n_tiles, r0 = (cut.ht - h * p.n_tiles) * kPagedRows;
-  const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;
-  int team = NW;  // warps per row
-  while (team > 1 && team * rows > NW) team /= 2;
-  const int per = NW / team;  // rows at a time
-  for (int base = 0; base < rows; base += per) {
-    const int row = base + warp / team, k = warp % team;
+  const int cta = static_cast<int>(blockIdx.x) / n_y, y = static_cast<int>(blockIdx.x) - cta * n_y;
+  PagedCut cut[kPagedWarps];
+  int n_cuts = 0;
+#pragma unroll
+  for (int w = 0; w < kPagedWarps; ++w) {
+    cut[w] = p.cuts[cta * kPagedWarps + w];
+    n_cuts += cut[w].n_parts > 0;
+  }
+  if (n_cuts == 0) return;
+  const int per_y = (p.R - y + n_y - 1) / n_y;  // rows of an item for this CTA
+  const int units = n_cuts * per_y;
+  int team = NW;                                // warps per (item, row)
+  while (team > 1 && team * units > NW) team /= 2;
+  const int per = NW / team, k = warp % team;
+  const bool mine = lane * VEC < D;
+  for (int base = 0; base < units; base += per) {
+    const int unit = base + warp / team;
+    int n = unit / per_y, row = y + (unit - n * per_y) * n_y, gw = -1;
+    PagedCut c{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kPagedWarps; ++w)
+      if (cut[w].n_parts > 0 && n-- == 0) {
+        c = cut[w];
+        gw = cta * kPagedWarps + w;
+      }
+    const int h = c.ht / p.n_tiles, r0 = (c.ht - h * p.n_tiles) * kPagedRows;
+    const bool in = unit < units && gw >= 0 && r0 + row < p.rows;
     float M = -INFINITY, L = 0.f, acc[VEC];
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) acc[c] = 0.f;
-    if (row < rows) {
-      for (int i = k; i < cut.n_parts; i += team) {
-        const long long at = (2LL * (gw + i) + (i == 0 ? 1 : 0)) * p.R + row;
-        const float2 ml = p.part_ml[at];
-        if (ml.y == 0.f) continue;  // no key seen (a NaN goes on)
-        float v[VEC];
-        const float* src = p.part_o + at * D + lane * VEC;
+    for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
+    if (in) {
+      for (int i0 = 32 * k; i0 < c.n_parts; i0 += 32 * team) {
+        const int i = i0 + lane;
+        const long long at = (2LL * (gw + i) + (i == 0)) * p.R + row;
+        const float2 ml = i < c.n_parts ? p.part_ml[at] : float2{-INFINITY, 0.f};
+        unsigned live = dec_ballot(ml.y != 0.f);  // (a NaN is live)
+        float m = ml.x;
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) v[c] = lane * VEC < D ? src[c] : 0.f;
-        const float m_new = fmaxf(M, ml.x), mu = m_new == -INFINITY ? 0.f : m_new;
-        const float fa = exp2f(M - mu), fb = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mu);
+        for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float m_new = fmaxf(M, m), mu = m_new == -INFINITY ? 0.f : m_new;
+        const float fa = exp2f(M - mu);
+        const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - mu);
+        float l = f * ml.y;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
         M = m_new;
-        L = fmaf(L, fa, fb * ml.y);
+        L = fmaf(L, fa, l);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[c] = fmaf(acc[c], fa, fb * v[c]);
-      }
-      float* mine = sh + warp * (2 + D);
-      if (lane == 0) {
-        mine[0] = M;
-        mine[1] = L;
-      }
+        for (int v = 0; v < VEC; ++v) acc[v] *= fa;
+        while (live != 0u) {
+          float x[ILP][VEC], w[ILP];
 #pragma unroll
-      for (int c = 0; c < VEC; ++c)
-        if (lane * VEC < D) mine[2 + lane * VEC + c] = acc[c];
+          for (int u = 0; u < ILP; ++u) {
+            const int src = live != 0u ? dec_lowest(live) : -1;
+            live &= live - 1u;
+            w[u] = dec_shfl(f, src < 0 ? 0 : src);
+            const long long a = (2LL * (gw + i0 + src) + (i0 + src == 0)) * p.R + row;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+              x[u][v] = src >= 0 && mine ? p.part_o[a * D + lane * VEC + v] : 0.f;
+            if (src < 0) w[u] = 0.f;
+          }
+#pragma unroll
+          for (int u = 0; u < ILP; ++u)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) acc[v] = fmaf(w[u], x[u][v], acc[v]);
+        }
+      }
+      if (k > 0) {
+        float* to = sh + warp * (2 + D);
+        if (lane == 0) {
+          to[0] = M;
+          to[1] = L;
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          if (mine) to[2 + lane * VEC + v] = acc[v];
+      }
     }
-    __syncthreads();
-    if (row < rows && k == 0) {
+    if (team > 1) __syncthreads();
+    if (in && k == 0) {
       for (int j = 1; j < team; ++j) {
-        const float* other = sh + (warp + j) * (2 + D);
-        const float mj = other[0], lj = other[1];
-        if (lj == 0.f) continue;
-        const float m_new = fmaxf(M, mj), mu = m_new == -INFINITY ? 0.f : m_new;
-        const float fa = exp2f(M - mu), fb = mj == -INFINITY ? 1.f : exp2f(mj - mu);
-        M = m_new;
-        L = fmaf(L, fa, fb * lj);
+        const float* from = sh + (warp + j) * (2 + D);
+        float fa, fb;
+        paged_join(from[0], from[1], M, L, fa, fb);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c)
-          if (lane * VEC < D) acc[c] = fmaf(acc[c], fa, fb * other[2 + lane * VEC + c]);
+        for (int v = 0; v < VEC; ++v)
+          acc[v] = fmaf(acc[v], fa, mine ? fb * from[2 + lane * VEC + v] : 0.f);
       }
       const int gr = r0 + row, gh = gr / p.Tq, t = gr - gh * p.Tq;
       const long long hq = static_cast<long long>(h) * (p.rows / p.Tq) + gh;
-      __nv_bfloat16* ob = p.o + cut.b * p.o_sb + hq * p.o_sh + t * p.o_st;
+      __nv_bfloat16* ob = p.o + c.b * p.o_sb + hq * p.o_sh + t * p.o_st;
       const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-      for (int c = 0; c < VEC; ++c)
-        if (lane * VEC < D) ob[lane * VEC + c] = __float2bfloat16_rn(acc[c] * inv);
+      for (int v = 0; v < VEC; ++v)
+        if (mine) ob[lane * VEC + v] = __float2bfloat16_rn(acc[v] * inv);
       if (lane == 0)
-        p.lse[(cut.b * static_cast<long long>(p.H) + hq) * p.Tq + t] =
-            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        p.lse[(c.b * static_cast<long long>(p.H) + hq) * p.Tq + t] = paged_lse(M, L);
     }
-    __syncthreads();
+    if (team > 1) __syncthreads();
   }
 }
 
 __host__ __device__ constexpr int paged_merge_smem_bytes(int D) {
   return kMergeThreads / 32 * (2 + D) * 4;
 }
+// CTAs of the merge per CTA of the decode: four rows of an item each.
+__host__ __device__ constexpr int paged_merge_y(int R) { return (R + 3) / 4; }
 
 }  // namespace cattn

@@ -56,8 +56,9 @@ static void put(const void* p, size_t bytes) {
 template <int D, bool UP>
 static void run_decode(const PagedParams& p, int grid) {
   emu::launch_ex(grid, kPagedThreads, paged_smem_bytes(D), 1, paged_decode_kernel<D, UP>, p);
-  emu::launch_ex(grid * kPagedWarps, kMergeThreads, paged_merge_smem_bytes(D), 1,
-                 paged_merge_kernel<D>, p);
+  const int n_y = paged_merge_y(p.R);
+  emu::launch_ex(grid * n_y, kMergeThreads, paged_merge_smem_bytes(D), 1, paged_merge_kernel<D>,
+                 p, n_y);
 }
 
 // params: B H Hkv Tq D n_pages P width n_sel grid layout; scale as float
