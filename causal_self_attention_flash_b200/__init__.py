@@ -20,7 +20,8 @@ import math
 
 import torch
 
-from ._binding import (ERR_CUDA, ERR_INVALID_ARG, ERR_TIMEOUT, ERR_TOO_LARGE,
+from ._binding import (CALL_CACHE_APPEND, CALL_DECODE_PAGED, CALL_DECODE_SPARSE, CALL_NAMES,
+                       CALL_PAGE_SELECT, CALL_PAGED_PLAN, CALL_WORDS, ERR_CUDA, ERR_INVALID_ARG, ERR_TIMEOUT, ERR_TOO_LARGE,
                        ERR_UNSUPPORTED, LIB, LIB_PATH, NOALLOC_SCRATCH_BYTES, OK,
                        CattnError, Dropout, Layout)
 
@@ -44,8 +45,15 @@ __all__ = [
 ]
 
 
+# the current stream's handle without a Stream object around it (0.1 us
+# against 3 us), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -455,36 +463,71 @@ def attn_decode(q, k, v, L, scale=None, o=None, lse=None, workspace=None, stream
     return o, lse
 
 
-def _array(t, dtype, shape, device, what):
-    """A contiguous device array of whole numbers or bounds; returns its
-    address."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected contiguous {dtype} of shape {shape}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{what}: expected a tensor on {device}")
+# The paged calls.  A step of a server makes them once per layer, so what
+# they cost in Python counts: each looks at a tensor's attributes once and
+# hands its arguments over as one array (attn_paged_call).
+
+_BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+
+
+def _device(t):
+    """The tensor's device, which has to be the current CUDA device."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    _same_device(t)
+    return t.device
+
+
+def _strides(t, dev, what, shape=None):
+    """Element strides of a bf16 view with unit last stride."""
+    st = t.stride()
+    if t.dtype != _BF16 or t.device != dev or not st or st[-1] != 1:
+        raise ValueError(f"{what}: expected a bf16 view on {dev} with unit last stride, "
+                         f"got {t.dtype} on {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return st
+
+
+def _array(t, dtype, shape, dev, what):
+    """The address of a contiguous device array."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _table(t, B, device):
-    """A block table: int32 (B, width) with unit last stride; returns its
-    address, row stride and width."""
-    if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] != B or t.stride(1) != 1:
-        raise ValueError("block_table: expected an int32 (B, width) tensor with unit last stride")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"block_table: expected a tensor on {device}")
-    width = t.shape[1]
-    return t.data_ptr(), t.stride(0) if B > 1 else width, width
+def _result(t, dtype, shape, dev, what):
+    """An output array, allocated if not given, and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _array(t, dtype, shape, dev, what)
 
 
-def _cache(k, v, D, device):
-    """(n_pages, Hkv, page_size) and layouts of the cache views."""
-    lk = _layout(k, torch.bfloat16, "k_cache", None, device)
-    lv = _layout(v, torch.bfloat16, "v_cache", k.shape, device)
-    n_pages, Hkv, P, Dk = k.shape
-    if Dk != D:
-        raise ValueError(f"k_cache: head size {Dk}, expected {D}")
-    return n_pages, Hkv, P, lk, lv
+def _table(t, B, dev):
+    """Address, row stride and width of an int32 (B, width) block table."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != B or t.dtype != _I32 or t.device != dev or st[1] != 1:
+        raise ValueError(f"block_table: expected an int32 ({B}, width) tensor on {dev} with unit "
+                         f"last stride, got {t.dtype} {tuple(shape)} on {t.device}")
+    return t.data_ptr(), st[0] if B > 1 else shape[1], shape[1]
+
+
+def _scratch(ws, dev, need):
+    """A workspace and its bytes; `need`: a function of no arguments."""
+    if ws is None:
+        ws = torch.empty(max(need(), 1), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous device memory on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _call(which, *words):
+    pack = CALL_WORDS[which]
+    st = LIB.attn_paged_call(which, pack.pack(*words), pack.size // 8)
+    if st != OK:
+        _check(CALL_NAMES[which], st)
 
 
 def attn_paged_plan(new_tokens, lengths, block_table, free_ring, ring_state, page_size, n_slots,
@@ -496,29 +539,23 @@ def attn_paged_plan(new_tokens, lengths, block_table, free_ring, ring_state, pag
     int64 (2).  Returns (lengths_out, ring_state_out, cu_new, slots,
     positions, status), all on the device; lengths_out and ring_state_out may
     be lengths and ring_state.  status is 0, or why nothing was changed."""
-    dev = new_tokens.device
+    dev = _device(new_tokens)
     B, n_pages = new_tokens.numel(), free_ring.numel()
-    i32, i64 = torch.int32, torch.int64
-    n_slots = int(n_slots)
     if n_slots < 0:
         raise ValueError("n_slots must not be negative")
-    p_new = _array(new_tokens, i32, (B,), dev, "new_tokens")
-    p_len = _array(lengths, i32, (B,), dev, "lengths")
+    p_new = _array(new_tokens, _I32, (B,), dev, "new_tokens")
+    p_len = _array(lengths, _I32, (B,), dev, "lengths")
     p_table, stride, width = _table(block_table, B, dev)
-    p_ring = _array(free_ring, i32, (n_pages,), dev, "free_ring")
-    p_state = _array(ring_state, i64, (2,), dev, "ring_state")
-    _same_device(new_tokens)
-    lengths_out = _want(lengths_out, new_tokens, i32, (B,))
-    ring_state_out = _want(ring_state_out, new_tokens, i64, (2,))
-    cu_new = _want(cu_new, new_tokens, i32, (B + 1,))
-    slots = _want(slots, new_tokens, i64, (n_slots,))
-    positions = _want(positions, new_tokens, i32, (n_slots,))
-    status = _want(status, new_tokens, i32, (1,))
-    st = LIB.attn_paged_plan(p_new, p_len, p_table, stride, p_ring, p_state, B, width, n_pages,
-                             int(page_size), n_slots, lengths_out.data_ptr(),
-                             ring_state_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-                             positions.data_ptr(), status.data_ptr(), _stream(stream))
-    _check("attn_paged_plan", st)
+    p_ring = _array(free_ring, _I32, (n_pages,), dev, "free_ring")
+    p_state = _array(ring_state, _I64, (2,), dev, "ring_state")
+    lengths_out, p_lo = _result(lengths_out, _I32, (B,), dev, "lengths_out")
+    ring_state_out, p_so = _result(ring_state_out, _I64, (2,), dev, "ring_state_out")
+    cu_new, p_cu = _result(cu_new, _I32, (B + 1,), dev, "cu_new")
+    slots, p_slots = _result(slots, _I64, (n_slots,), dev, "slots")
+    positions, p_pos = _result(positions, _I32, (n_slots,), dev, "positions")
+    status, p_st = _result(status, _I32, (1,), dev, "status")
+    _call(CALL_PAGED_PLAN, p_new, p_len, p_table, stride, p_ring, p_state, B, width, n_pages,
+          page_size, n_slots, p_lo, p_so, p_cu, p_slots, p_pos, p_st, _stream(stream))
     return lengths_out, ring_state_out, cu_new, slots, positions, status
 
 
@@ -528,58 +565,57 @@ def attn_cache_append(k_new, v_new, k_cache, v_cache, slots, bounds=None, stream
     bf16 (n_pages, Hkv, page_size, D) views.  bounds, bf16 (n_pages, Hkv, 2,
     D): the pages' lowest and highest key values, kept up to date for
     attn_page_select."""
-    n, Hn, D = k_new.shape
-    dev = k_new.device
-    n_pages, Hkv, P, lk, lv = _cache(k_cache, v_cache, D, dev)
-    if Hn != Hkv or v_new.shape != k_new.shape:
-        raise ValueError(f"k_new, v_new: expected (n, {Hkv}, {D})")
-    for t, what in ((k_new, "k_new"), (v_new, "v_new")):
-        if t.dtype != torch.bfloat16 or t.stride(2) != 1 or not t.is_cuda or t.device != dev:
-            raise ValueError(f"{what}: expected a bf16 view on {dev} with unit last stride")
-    p_slots = _array(slots, torch.int64, (n,), dev, "slots")
-    p_bounds = None
+    dev = _device(k_new)
+    cache = k_cache.shape
+    if len(cache) != 4:
+        raise ValueError("k_cache: expected a (n_pages, Hkv, page_size, D) view")
+    n_pages, Hkv, P, D = cache
+    n = slots.numel()
+    skn = _strides(k_new, dev, "k_new", (n, Hkv, D))
+    svn = _strides(v_new, dev, "v_new", (n, Hkv, D))
+    sk = _strides(k_cache, dev, "k_cache")
+    sv = _strides(v_cache, dev, "v_cache", cache)
+    p_slots = _array(slots, _I64, (n,), dev, "slots")
+    p_bounds = 0
     if bounds is not None:
-        p_bounds = _array(bounds, torch.bfloat16, (n_pages, Hkv, 2, D), dev, "bounds")
-    _same_device(k_new)
-    st = LIB.attn_cache_append(k_new.data_ptr(), Layout(8, k_new.stride(1), k_new.stride(0)),
-                               v_new.data_ptr(), Layout(8, v_new.stride(1), v_new.stride(0)),
-                               n, Hkv, D, n_pages, P, p_slots, k_cache.data_ptr(), lk,
-                               v_cache.data_ptr(), lv, p_bounds, _stream(stream))
-    _check("attn_cache_append", st)
+        p_bounds = _array(bounds, _BF16, (n_pages, Hkv, 2, D), dev, "bounds")
+    _call(CALL_CACHE_APPEND, k_new.data_ptr(), 0, skn[1], skn[0], v_new.data_ptr(), 0, svn[1],
+          svn[0], n, Hkv, D, n_pages, P, p_slots, k_cache.data_ptr(), sk[0], sk[1], sk[2],
+          v_cache.data_ptr(), sv[0], sv[1], sv[2], p_bounds, _stream(stream))
 
 
 def attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D):
     return int(LIB.attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D))
 
 
-def _decode_paged(name, q, k_cache, v_cache, block_table, lengths, pages, scale, o, lse,
+def _decode_paged(which, q, k_cache, v_cache, block_table, lengths, pages, scale, o, lse,
                   workspace, stream):
-    B, H, Tq, D = _shape(q)
-    dev = q.device
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    lq = _layout(q, torch.bfloat16, "q", None, dev)
-    n_pages, Hkv, P, lk, lv = _cache(k_cache, v_cache, D, dev)
+    dev = _device(q)
+    shape, cache = q.shape, k_cache.shape
+    if len(shape) != 4 or len(cache) != 4 or cache[3] != shape[3]:
+        raise ValueError(f"expected q (B, H, Tq, D) and a (n_pages, Hkv, page_size, D) cache, got "
+                         f"{tuple(shape)} and {tuple(cache)}")
+    B, H, Tq, D = shape
+    n_pages, Hkv, P, _ = cache
+    sq = _strides(q, dev, "q")
+    sk = _strides(k_cache, dev, "k_cache")
+    sv = _strides(v_cache, dev, "v_cache", cache)
     p_table, stride, width = _table(block_table, B, dev)
-    p_len = _array(lengths, torch.int32, (B,), dev, "lengths")
+    p_len = _array(lengths, _I32, (B,), dev, "lengths")
     listed = ()
     if pages is not None:
         K = pages.shape[-1]
-        listed = (_array(pages, torch.int32, (B, Hkv, K), dev, "pages"), K)
-    _same_device(q)
+        listed = (_array(pages, _I32, (B, Hkv, K), dev, "pages"), K)
     if o is None:
-        o = torch.empty((B, H, Tq, D), dtype=torch.bfloat16, device=dev)
-    lo = _layout(o, torch.bfloat16, "o", (B, H, Tq, D), dev)
-    lse = _want(lse, q, torch.float32, (B, H, Tq))
-    if workspace is None:
-        workspace = _workspace(None, q, attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D))
-    else:
-        _workspace(workspace, q, 0)
-    st = getattr(LIB, name)(q.data_ptr(), lq, k_cache.data_ptr(), lk, v_cache.data_ptr(), lv,
-                            float(scale), B, H, Hkv, Tq, D, n_pages, P, p_table, stride, width,
-                            p_len, *listed, o.data_ptr(), lo, lse.data_ptr(),
-                            workspace.data_ptr(), _nbytes(workspace), _stream(stream))
-    _check(name, st)
+        o = torch.empty(shape, dtype=_BF16, device=dev)
+    so = _strides(o, dev, "o", shape)
+    lse, p_lse = _result(lse, _F32, (B, H, Tq), dev, "lse")
+    p_ws, ws_bytes = _scratch(workspace, dev,
+                              lambda: attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D))
+    _call(which, q.data_ptr(), sq[0], sq[1], sq[2], k_cache.data_ptr(), sk[0], sk[1], sk[2],
+          v_cache.data_ptr(), sv[0], sv[1], sv[2], D ** -0.5 if scale is None else scale, B, H,
+          Hkv, Tq, D, n_pages, P, p_table, stride, width, p_len, *listed, o.data_ptr(), so[0],
+          so[1], so[2], p_lse, p_ws, ws_bytes, _stream(stream))
     return o, lse
 
 
@@ -593,15 +629,15 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, lengths, scale=None, o=N
     fp32; rows that see no key give 0 and -inf.  workspace: a uint8 CUDA
     tensor of attn_decode_paged_workspace_bytes bytes, allocated if not
     given."""
-    return _decode_paged("attn_decode_paged", q, k_cache, v_cache, block_table, lengths, None,
-                         scale, o, lse, workspace, stream)
+    return _decode_paged(CALL_DECODE_PAGED, q, k_cache, v_cache, block_table, lengths, None, scale,
+                         o, lse, workspace, stream)
 
 
 def attn_decode_sparse(q, k_cache, v_cache, block_table, lengths, pages, scale=None, o=None,
                        lse=None, workspace=None, stream=None):
     """attn_decode_paged over the listed pages only: pages int32 (B, Hkv, K)
     as attn_page_select gives them."""
-    return _decode_paged("attn_decode_sparse", q, k_cache, v_cache, block_table, lengths, pages,
+    return _decode_paged(CALL_DECODE_SPARSE, q, k_cache, v_cache, block_table, lengths, pages,
                          scale, o, lse, workspace, stream)
 
 
@@ -615,26 +651,23 @@ def attn_page_select(q, bounds, block_table, lengths, page_size, n_select, n_fir
     (see attn_cache_append) promise the largest scores for the query rows q
     bf16 (B, H, Tq, D), the n_first first and n_last last among them; int32
     (B, Hkv, n_select), ascending, -1 behind the last."""
-    B, H, Tq, D = _shape(q)
-    dev = q.device
-    lq = _layout(q, torch.bfloat16, "q", None, dev)
-    if bounds.dim() != 4:
-        raise ValueError("bounds: expected (n_pages, Hkv, 2, D)")
-    n_pages, Hkv = bounds.shape[0], bounds.shape[1]
-    p_bounds = _array(bounds, torch.bfloat16, (n_pages, Hkv, 2, D), dev, "bounds")
+    dev = _device(q)
+    shape, bs = q.shape, bounds.shape
+    if len(shape) != 4 or len(bs) != 4:
+        raise ValueError(f"expected q (B, H, Tq, D) and bounds (n_pages, Hkv, 2, D), got "
+                         f"{tuple(shape)} and {tuple(bs)}")
+    B, H, Tq, D = shape
+    n_pages, Hkv = bs[0], bs[1]
+    sq = _strides(q, dev, "q")
+    p_bounds = _array(bounds, _BF16, (n_pages, Hkv, 2, D), dev, "bounds")
     p_table, stride, width = _table(block_table, B, dev)
-    p_len = _array(lengths, torch.int32, (B,), dev, "lengths")
-    _same_device(q)
-    pages = _want(pages, q, torch.int32, (B, Hkv, int(n_select)))
-    if workspace is None:
-        workspace = _workspace(None, q, attn_page_select_workspace_bytes(B, Hkv, width))
-    else:
-        _workspace(workspace, q, 0)
-    st = LIB.attn_page_select(q.data_ptr(), lq, p_bounds, B, H, Hkv, Tq, D, n_pages,
-                              int(page_size), p_table, stride, width, p_len, int(n_select),
-                              int(n_first), int(n_last), pages.data_ptr(), workspace.data_ptr(),
-                              _nbytes(workspace), _stream(stream))
-    _check("attn_page_select", st)
+    p_len = _array(lengths, _I32, (B,), dev, "lengths")
+    pages, p_pages = _result(pages, _I32, (B, Hkv, n_select), dev, "pages")
+    p_ws, ws_bytes = _scratch(workspace, dev,
+                              lambda: attn_page_select_workspace_bytes(B, Hkv, width))
+    _call(CALL_PAGE_SELECT, q.data_ptr(), sq[0], sq[1], sq[2], p_bounds, B, H, Hkv, Tq, D, n_pages,
+          page_size, p_table, stride, width, p_len, n_select, n_first, n_last, p_pages, p_ws,
+          ws_bytes, _stream(stream))
     return pages
 
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcattn.so")
@@ -79,6 +80,7 @@ SIGNATURES = {
                               _i, _vp, _vp, _sz, _vp]),
     "attn_decode_sparse": (_i, [_vp, _L, _vp, _L, _vp, _L, _f, _i, _i, _i, _i, _i, _i, _i, _vp,
                                 _ll, _i, _vp, _vp, _i, _vp, _L, _vp, _vp, _sz, _vp]),
+    "attn_paged_call": (_i, [_i, ctypes.c_char_p, _i]),
     "cattn_get_device_status": (_i, [_i, _vp]),
     "cattn_set_wait_timeout_us": (None, [_u32]),
     "cattn_selftest_wait_timeout": (_i, [_u32, _vp]),
@@ -91,6 +93,14 @@ SIGNATURES = {
     "cattn_plan_passes": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_uint16), _i]),
     "cattn_last_cuda_error": (_i, []),
 }
+
+
+# attn_paged_call: the paged calls by number, and their words ("q" whole
+# numbers and addresses, "d" the scale)
+CALL_PAGED_PLAN, CALL_CACHE_APPEND, CALL_DECODE_PAGED, CALL_PAGE_SELECT, CALL_DECODE_SPARSE = range(5)
+CALL_NAMES = ("attn_paged_plan", "attn_cache_append", "attn_decode_paged", "attn_page_select",
+              "attn_decode_sparse")
+CALL_WORDS = tuple(struct.Struct(f) for f in ("=18q", "=24q", "=12qd19q", "=23q", "=12qd21q"))
 
 
 class CattnError(RuntimeError):

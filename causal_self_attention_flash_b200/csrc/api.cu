@@ -1175,6 +1175,121 @@ cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds
   return CATTN_ERR_UNSUPPORTED;
 }
 
+cattn_status attn_paged_call(int call, const int64_t* words, int n) {
+  static const int counts[] = {18, 24, 32, 23, 34};
+  if (call < 0 || call > 4 || n != counts[call] || !words) return CATTN_ERR_INVALID_ARG;
+  const int64_t* w = words;
+  bool fits = true;
+  auto num = [&]() {
+    const int64_t x = *w++;
+    fits = fits && x == static_cast<int>(x);
+    return static_cast<int>(x);
+  };
+  auto big = [&]() { return static_cast<long long>(*w++); };
+  auto layout = [&]() {
+    const cattn_layout l{w[0], w[1], w[2]};
+    w += 3;
+    return l;
+  };
+  auto real = [&]() {
+    double x;
+    memcpy(&x, w++, 8);
+    return static_cast<float>(x);
+  };
+  auto bytes = [&]() { return static_cast<size_t>(*w++); };
+  auto ptr = [&]() { return reinterpret_cast<void*>(static_cast<uintptr_t>(*w++)); };
+  auto i32 = [&]() { return static_cast<int32_t*>(ptr()); };
+  auto i64 = [&]() { return static_cast<int64_t*>(ptr()); };
+  switch (call) {
+    case CATTN_CALL_PAGED_PLAN: {
+      const int32_t *asked = i32(), *lengths = i32();
+      int32_t* table = i32();
+      const long long stride = big();
+      int32_t* ring = i32();
+      const int64_t* state = i64();
+      const int B = num(), width = num(), n_pages = num(), P = num();
+      const long long n_slots = big();
+      int32_t* lengths_out = i32();
+      int64_t* state_out = i64();
+      int32_t* cu = i32();
+      int64_t* slots = i64();
+      int32_t *positions = i32(), *status = i32();
+      void* stream = ptr();
+      if (!fits) return CATTN_ERR_INVALID_ARG;
+      return attn_paged_plan(asked, lengths, table, stride, ring, state, B, width, n_pages, P,
+                             n_slots, lengths_out, state_out, cu, slots, positions, status, stream);
+    }
+    case CATTN_CALL_CACHE_APPEND: {
+      const void* kn = ptr();
+      const cattn_layout lkn = layout();
+      const void* vn = ptr();
+      const cattn_layout lvn = layout();
+      const long long rows = big();
+      const int Hkv = num(), D = num(), n_pages = num(), P = num();
+      const int64_t* slots = i64();
+      void* k = ptr();
+      const cattn_layout lk = layout();
+      void* v = ptr();
+      const cattn_layout lv = layout();
+      void* bounds = ptr();
+      void* stream = ptr();
+      if (!fits) return CATTN_ERR_INVALID_ARG;
+      return attn_cache_append(kn, lkn, vn, lvn, rows, Hkv, D, n_pages, P, slots, k, lk, v, lv,
+                               bounds, stream);
+    }
+    case CATTN_CALL_PAGE_SELECT: {
+      const void* q = ptr();
+      const cattn_layout lq = layout();
+      const void* bounds = ptr();
+      const int B = num(), H = num(), Hkv = num(), Tq = num(), D = num(), n_pages = num(),
+                P = num();
+      const int32_t* table = i32();
+      const long long stride = big();
+      const int width = num();
+      const int32_t* lengths = i32();
+      const int K = num(), n_first = num(), n_last = num();
+      int32_t* pages = i32();
+      void* ws = ptr();
+      const size_t ws_bytes = bytes();
+      void* stream = ptr();
+      if (!fits) return CATTN_ERR_INVALID_ARG;
+      return attn_page_select(q, lq, bounds, B, H, Hkv, Tq, D, n_pages, P, table, stride, width,
+                              lengths, K, n_first, n_last, pages, ws, ws_bytes, stream);
+    }
+    default: {  // CATTN_CALL_DECODE_PAGED, CATTN_CALL_DECODE_SPARSE
+      const bool sparse = call == CATTN_CALL_DECODE_SPARSE;
+      const void* q = ptr();
+      const cattn_layout lq = layout();
+      const void* k = ptr();
+      const cattn_layout lk = layout();
+      const void* v = ptr();
+      const cattn_layout lv = layout();
+      const float scale = real();
+      const int B = num(), H = num(), Hkv = num(), Tq = num(), D = num(), n_pages = num(),
+                P = num();
+      const int32_t* table = i32();
+      const long long stride = big();
+      const int width = num();
+      const int32_t* lengths = i32();
+      const int32_t* pages = sparse ? i32() : nullptr;
+      const int K = sparse ? num() : 0;
+      void* o = ptr();
+      const cattn_layout lo = layout();
+      float* lse = static_cast<float*>(ptr());
+      void* ws = ptr();
+      const size_t ws_bytes = bytes();
+      void* stream = ptr();
+      if (!fits) return CATTN_ERR_INVALID_ARG;
+      return sparse ? attn_decode_sparse(q, lq, k, lk, v, lv, scale, B, H, Hkv, Tq, D, n_pages, P,
+                                         table, stride, width, lengths, pages, K, o, lo, lse, ws,
+                                         ws_bytes, stream)
+                    : attn_decode_paged(q, lq, k, lk, v, lv, scale, B, H, Hkv, Tq, D, n_pages, P,
+                                        table, stride, width, lengths, o, lo, lse, ws, ws_bytes,
+                                        stream);
+    }
+  }
+}
+
 size_t attn_bwd_workspace_bytes(int B, int H, int T, int D) {
   if (check_shape(B, H, T, D) != CATTN_OK) return 0;
   if (empty_shape(B, H, T)) return 0;

@@ -481,6 +481,27 @@ CATTN_API cattn_status attn_decode_sparse(const void* q, cattn_layout lq, const 
                                           int n_select, void* o, cattn_layout lo, float* lse,
                                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* The calls on a paged cache with their arguments in an array of 64-bit
+ * words, for bindings that pay for each argument (from Python, a call with
+ * one array takes 2 us less than one with 24 arguments).
+ *
+ *   call   which one
+ *   words  its parameters in their order: pointers and whole numbers as
+ *          they are, a cattn_layout as its three numbers, scale as the bits
+ *          of a double
+ *   n      their number
+ *
+ * Returns what the call itself returns; CATTN_ERR_INVALID_ARG for an unknown
+ * call, a wrong n, or a word that does not fit its parameter. */
+enum {
+  CATTN_CALL_PAGED_PLAN = 0,   /* attn_paged_plan, 18 words */
+  CATTN_CALL_CACHE_APPEND = 1, /* attn_cache_append, 24 words */
+  CATTN_CALL_DECODE_PAGED = 2, /* attn_decode_paged, 32 words */
+  CATTN_CALL_PAGE_SELECT = 3,  /* attn_page_select, 23 words */
+  CATTN_CALL_DECODE_SPARSE = 4 /* attn_decode_sparse, 34 words */
+};
+CATTN_API cattn_status attn_paged_call(int call, const int64_t* words, int n);
+
 /* Backward pass for callers that cannot allocate device memory.
  *
  * Same computation, arguments and results as attn_bwd, minus the workspace:
