@@ -1123,7 +1123,7 @@ cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
 
 size_t attn_page_select_workspace_bytes(int B, int Hkv, int width) {
   if (B <= 0 || Hkv <= 0 || width <= 0) return 0;
-  return static_cast<size_t>(B) * Hkv * width * sizeof(double);
+  return static_cast<size_t>(select_workspace_bytes(static_cast<long long>(B) * Hkv, width));
 }
 
 cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds, int B, int H,
@@ -1148,7 +1148,8 @@ cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds
       (!workspace || workspace_bytes < attn_page_select_workspace_bytes(B, Hkv, width)))
     return CATTN_ERR_INVALID_ARG;
   SelectParams p;
-  p.n_blocks = (width + kScorePages - 1) / kScorePages;
+  p.n_blocks = (width + score_pages(D) - 1) / score_pages(D);
+  p.D = D;
   const long long bh = static_cast<long long>(B) * Hkv;
   if (bh * p.n_blocks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
   int dev;
@@ -1164,7 +1165,9 @@ cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds
   p.n_pages = n_pages; p.P = page_size; p.width = width;
   p.n_sel = n_select; p.n_first = n_first; p.n_last = n_last;
   p.pages = pages;
-  p.score = static_cast<double*>(workspace);
+  p.exact = static_cast<double*>(workspace);
+  p.score = reinterpret_cast<float*>(p.exact + bh * width);
+  p.largest = p.score + bh * width;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (D) {
     case 16: return select_impl<16>(p, s);

@@ -319,9 +319,19 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 // order, -1 behind the last.  A page that is not held has s = -inf, a NaN
 // counts as +inf.
 //
-// The scores are exact to 64 bits, so that the choice does not depend on an
-// order of summation (a product of two bf16 values has 16 bits, so a sum of
-// 2 D of them is exact unless they span more than 2^29).
+// The choice is that of exact sums, so that it does not depend on an order of
+// summation.  page_score_kernel sums in fp32: at most 13 roundings lie on the
+// way of a term (8 products in a lane, 5 additions between lanes), so with
+// V = the largest |bound| of the request's pages and u = 2^-24
+//   |s_i - exact| <= 14 u max_r sum_d |q_rd| V = rho.
+// The want-th highest of a list moves by at most rho if every entry does, so
+// a page more than 2 rho above (below) the want-th highest fp32 score T is
+// chosen (is not).  Only if more pages lie within 2 rho of T than there are
+// places left for, page_pick_kernel sums those again in 64 bits (a product of
+// two bf16 values has 16 bits: a sum of 2 D of them is exact there unless they
+// span more than 2^29).
+//
+// The bound is memory: 4 D bytes per page and cache head, read once.
 
 struct SelectParams {
   const __nv_bfloat16* q;       // (B, H, Tq, D)
@@ -330,15 +340,24 @@ struct SelectParams {
   const int* table;
   long long table_sb;
   const int* lengths;
-  int B, H, Hkv, Tq, rows, n_pages, P, width, n_sel, n_first, n_last;
-  int n_blocks;                 // ceil(width / kScorePages)
+  int B, H, Hkv, Tq, D, rows, n_pages, P, width, n_sel, n_first, n_last;
+  int n_blocks;                 // ceil(width / score_pages(D))
   int* pages;                   // (B, Hkv, n_sel)
-  double* score;                // [B][Hkv][width]
+  double* exact;                // [B Hkv][width]
+  float* score;                 // [B Hkv][width]
+  float* largest;               // [B Hkv][n_blocks][score warps]: |bounds|
 };
 
 constexpr int kScoreThreads = 128;
-constexpr int kScorePages = 32;    // pages per CTA
-constexpr int kPickThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreLoads = 8;     // 16-byte loads of a lane in flight
+constexpr int kScoreRows = 4;      // query rows at a time
+constexpr int kPickThreads = 512;
+constexpr int kPickKeys = 8192;    // scores kept in shared memory
+
+// Pages of a warp and of a CTA: a page's bounds are 4 D bytes, D / 4 lanes.
+__host__ __device__ constexpr int score_warp_pages(int D) { return kScoreLoads * 128 / D; }
+__host__ __device__ constexpr int score_pages(int D) { return kScoreWarps * score_warp_pages(D); }
 
 __device__ __forceinline__ int select_count(const SelectParams& p, int b) {
   const int len = p.lengths[b];
@@ -346,133 +365,369 @@ __device__ __forceinline__ int select_count(const SelectParams& p, int b) {
   return n < p.width ? n : p.width;
 }
 
-// Grid: B * Hkv * n_blocks.  Warp: a page at a time.
+__device__ __forceinline__ const __nv_bfloat16* select_row(const SelectParams& p, int b, int h,
+                                                           int r) {
+  const int gh = r / p.Tq, t = r - gh * p.Tq;
+  return p.q + b * p.q_sb + (static_cast<long long>(h) * (p.rows / p.Tq) + gh) * p.q_sh +
+         t * p.q_st;
+}
+
+// Grid: B * Hkv * n_blocks.  A warp takes score_warp_pages(D) pages, all of
+// whose bounds are on their way at once; a lane holds 8 channels of lo or hi
+// of one page per load, and of up to four query rows.
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectParams p) {
+  constexpr int LP = D / 4;                 // lanes per page
+  constexpr int PW = score_warp_pages(D);
+  constexpr int NV = kScoreLoads * kScoreRows / LP;  // sums that a lane ends up with
+  constexpr int KEPT = NV > 0 ? NV : 1;
+  static_assert(kScoreLoads * kScoreRows == 32, "one sum per lane at D = 128");
   dec_grid_dep_wait();
   dec_grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bh = static_cast<int>(blockIdx.x) / p.n_blocks;
+  const int blk = static_cast<int>(blockIdx.x) - bh * p.n_blocks;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int count = select_count(p, b);
   if (count <= p.n_sel) return;  // every page is taken
-  const int first = (static_cast<int>(blockIdx.x) - bh * p.n_blocks) * kScorePages;
-  constexpr int CPL = D / 16;    // channels per lane and bound, 16 lanes
-  for (int i = first + warp; i < first + kScorePages && i < count; i += kScoreThreads / 32) {
-    const int page = p.table[b * p.table_sb + i];
-    double best = -INFINITY;
-    if (page >= 0 && page < p.n_pages) {
-      // lanes 0-15 take hi, 16-31 lo
-      const bool low = lane >= 16;
-      const __nv_bfloat16* src =
-          p.bounds + ((static_cast<long long>(page) * p.Hkv + h) * 2 + (low ? 0 : 1)) * D +
-          (lane & 15) * CPL;
-      float v[CPL];
+  const int first = blk * score_pages(D) + warp * PW;
+  if (blk * score_pages(D) >= count) return;
+  const int lp = lane % LP;           // the lane's place in its page: lo first
+  const bool low = lp < LP / 2;
+  const int ch = (lp % (LP / 2)) * 8;
+  // the warp's pages, one or more per lane; -1: not held
+  uint4 v[kScoreLoads];
+  float big = 0.f;
+  constexpr int TL = (PW + 31) / 32;
+  int pg[TL];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) v[c] = __bfloat162float(src[c]);
-      for (int r = 0; r < p.rows; ++r) {
-        const int gh = r / p.Tq, t = r - gh * p.Tq;
-        const __nv_bfloat16* qr = p.q + b * p.q_sb +
-                                  (static_cast<long long>(h) * (p.rows / p.Tq) + gh) * p.q_sh +
-                                  t * p.q_st + (lane & 15) * CPL;
-        double s = 0.0;
+  for (int i = 0; i < TL; ++i) {
+    const int at = first + 32 * i + lane;
+    pg[i] = 32 * i + lane < PW && at < count ? p.table[b * p.table_sb + at] : -1;
+    if (pg[i] >= p.n_pages) pg[i] = -1;
+  }
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-          const float x = __bfloat162float(qr[c]);
-          const float y = low ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);  // (NaN stays)
-          s += static_cast<double>(y) * static_cast<double>(v[c]);
+  for (int j = 0; j < kScoreLoads; ++j) {
+    constexpr int PPL = 32 / LP;      // pages per load
+    const int i = j * PPL;            // compile-time register, lane within it
+    const int page = dec_shfl(pg[i / 32], i % 32 + lane / LP);
+    v[j] = page < 0 ? uint4{0, 0, 0, 0}
+                    : *reinterpret_cast<const uint4*>(
+                          p.bounds + ((static_cast<long long>(page) * p.Hkv + h) * 2 + !low) * D +
+                          ch);
+  }
+#pragma unroll
+  for (int j = 0; j < kScoreLoads; ++j) {
+    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      big = fmaxf(big, fmaxf(fabsf(dec_bf16_lo(w[c])), fabsf(dec_bf16_hi(w[c]))));
+  }
+  float best[KEPT];
+#pragma unroll
+  for (int i = 0; i < KEPT; ++i) best[i] = -INFINITY;
+  for (int r0 = 0; r0 < p.rows; r0 += kScoreRows) {
+    float s[kScoreLoads * kScoreRows];
+    // four rows in turn (past the last: the last again)
+#pragma unroll
+    for (int r = 0; r < kScoreRows; ++r) {
+      const uint4 qw = *reinterpret_cast<const uint4*>(
+          select_row(p, b, h, r0 + r < p.rows ? r0 + r : p.rows - 1) + ch);
+      const uint32_t w[4] = {qw.x, qw.y, qw.z, qw.w};
+      float y[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float x = (c & 1) ? dec_bf16_hi(w[c / 2]) : dec_bf16_lo(w[c / 2]);
+        y[c] = low ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);  // (a NaN stays)
+      }
+#pragma unroll
+      for (int j = 0; j < kScoreLoads; ++j) {
+        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        float a = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          a = fmaf(y[2 * c], dec_bf16_lo(u[c]), a);
+          a = fmaf(y[2 * c + 1], dec_bf16_hi(u[c]), a);
         }
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) s += dec_shfl(s, lane ^ d);
-        if (s != s) s = INFINITY;
-        best = s > best ? s : best;
+        s[j * kScoreRows + r] = a;
       }
     }
-    if (lane == 0) p.score[static_cast<long long>(bh) * p.width + i] = best;
+    // sums over the LP lanes of a page: at each step a lane hands half of its
+    // values to its partner and takes the other half's, so that lane lp ends
+    // with values lp NV .. lp NV + NV - 1
+#pragma unroll
+    for (int d = LP / 2, n = kScoreLoads * kScoreRows / 2; d > 0; d /= 2, n /= 2) {
+      const bool upper = (lane & d) != 0;
+#pragma unroll
+      for (int i = 0; i < kScoreLoads * kScoreRows / 2; ++i)
+        if (i < n) {
+          const float keep = upper ? s[i + n] : s[i], give = upper ? s[i] : s[i + n];
+          s[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+        }
+    }
+    // a sum that is not finite is left to the exact pass: +inf marks it
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i) best[i] = s[i] - s[i] == 0.f ? fmaxf(best[i], s[i]) : INFINITY;
   }
+  // the highest of the four rows: values of one lane, or of 4 / NV lanes
+  constexpr int RL = KEPT < kScoreRows ? KEPT : kScoreRows;
+  float* out = p.score + static_cast<long long>(bh) * p.width;
+#pragma unroll
+  for (int i = 0; i < KEPT; i += RL) {
+    float m = best[i];
+#pragma unroll
+    for (int r = 1; r < RL; ++r) m = fmaxf(m, best[i + r]);
+#pragma unroll
+    for (int d = 1; d < kScoreRows / RL; d *= 2)
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const int value = lp * KEPT + i;  // of the lane's page group
+    const int at = (value / kScoreRows) * (32 / LP) + lane / LP;
+    // whether the page is held: from the lane that looked it up
+    int page = -1;
+#pragma unroll
+    for (int t = 0; t < TL; ++t) {
+      const int x = dec_shfl(pg[t], at % 32);
+      if (at / 32 == t) page = x;
+    }
+    if (value % kScoreRows == 0 && first + at < count) out[first + at] = page < 0 ? -INFINITY : m;
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+  if (lane == 0)
+    p.largest[(static_cast<long long>(bh) * p.n_blocks + blk) * kScoreWarps + warp] = big;
 }
 
 // Whole numbers in the order of the scores (both zeros alike).
+__device__ __forceinline__ unsigned score_key(float s) {
+  const unsigned u = dec_float_bits(s + 0.f);
+  return (u >> 31) ? ~u : u | (1u << 31);
+}
 __device__ __forceinline__ unsigned long long score_key(double s) {
   const unsigned long long u = static_cast<unsigned long long>(dec_double_bits(s + 0.0));
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
-// Grid: B * Hkv CTAs.  Radix select, eight bits at a time.
+// Sums of the N values v over the CTA's threads; `sh` has two halves of three
+// words per warp, used in turn, so that one barrier is enough.
+template <int N>
+__device__ __forceinline__ void pick_sums(int (&v)[N], int* sh, int& turn) {
+  constexpr int NW = kPickThreads / 32;
+  static_assert(N <= 3 && NW <= 32, "sums");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int* half = sh + turn * 3 * NW;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = dec_warp_sum(v[i]);
+    if (lane == 0) half[i * NW + warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dec_warp_sum(lane < NW ? half[i * NW + lane] : 0);
+  turn ^= 1;
+}
+// The highest digit 0 .. 3 that at least `want` keys reach; n: how many reach
+// 1, 2 and 3.
+__device__ __forceinline__ unsigned pick_digit(const int (&n)[3], int want) {
+  return n[2] >= want ? 3u : n[1] >= want ? 2u : n[0] >= want ? 1u : 0u;
+}
+
+// Exact score of page i (a warp): the largest row's, in 64 bits; a NaN as +inf.
+__device__ __forceinline__ double exact_score(const SelectParams& p, int b, int h, int i) {
+  const int lane = threadIdx.x & 31;
+  const int page = p.table[b * p.table_sb + i];
+  double best = -INFINITY;
+  if (page < 0 || page >= p.n_pages) return best;
+  const __nv_bfloat16* lo = p.bounds + (static_cast<long long>(page) * p.Hkv + h) * 2 * p.D;
+  for (int r = 0; r < p.rows; ++r) {
+    const __nv_bfloat16* q = select_row(p, b, h, r);
+    double s = 0.0;
+    for (int d = lane; d < p.D; d += 32) {
+      const float x = __bfloat162float(q[d]);
+      const float up = x < 0.f ? 0.f : x, down = x > 0.f ? 0.f : x;
+      s += static_cast<double>(up) * static_cast<double>(__bfloat162float(lo[p.D + d]));
+      s += static_cast<double>(down) * static_cast<double>(__bfloat162float(lo[d]));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) s += dec_shfl(s, lane ^ d);
+    if (s != s) s = INFINITY;
+    best = s > best ? s : best;
+  }
+  return best;
+}
+
+// Grid: B * Hkv CTAs of kPickThreads.
 __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
+  constexpr int NW = kPickThreads / 32;
   dec_grid_dep_wait();
   dec_grid_dep_launch();
-  int* sh = reinterpret_cast<int*>(dec_dynamic_smem());
-  int* hist = sh;             // [256]
-  int* found = sh + 256;      // digit, how many are still wanted
-  int* sums = sh + 258;       // [2][warps]
+  unsigned* keys = reinterpret_cast<unsigned*>(dec_dynamic_smem());  // [kPickKeys]
+  int* sh = reinterpret_cast<int*>(keys + kPickKeys);                // [2][3][NW]
+  float* shf = reinterpret_cast<float*>(sh + 6 * NW);                // [2][NW]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = static_cast<int>(blockIdx.x) / p.Hkv;
+  const int bh = static_cast<int>(blockIdx.x), b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int count = select_count(p, b);
-  int* out = p.pages + static_cast<long long>(blockIdx.x) * p.n_sel;
+  int* out = p.pages + static_cast<long long>(bh) * p.n_sel;
   if (count <= p.n_sel) {
     for (int i = tid; i < p.n_sel; i += kPickThreads) out[i] = i < count ? i : -1;
     return;
   }
-  const double* score = p.score + static_cast<long long>(blockIdx.x) * p.width;
+  const float* score = p.score + static_cast<long long>(bh) * p.width;
+  double* exact = p.exact + static_cast<long long>(bh) * p.width;
   const int lo = p.n_first, hi = count - p.n_last;  // candidates: lo <= i < hi
-  int want = p.n_sel - p.n_first - p.n_last;
-  unsigned long long prefix = 0;  // the digits of the want-th highest key so far
-  for (int shift = 56; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (int i = lo + tid; i < hi; i += kPickThreads) {
-      const unsigned long long k = score_key(score[i]);
-      if (shift == 56 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        dec_add_shared(&hist[(k >> shift) & 255], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int digit = 255, above = 0;
-      while (digit > 0 && above + hist[digit] < want) above += hist[digit--];
-      found[0] = digit;
-      found[1] = want - above;
-    }
-    __syncthreads();
-    prefix |= static_cast<unsigned long long>(found[0]) << shift;
-    want = found[1];
-    __syncthreads();
+  int want = p.n_sel - p.n_first - p.n_last, turn = 0;
+
+  // rho: the largest |bound| and the largest sum |q| of a row
+  float big = 0.f, qsum = 0.f;
+  const int n_big = (count + score_pages(p.D) - 1) / score_pages(p.D) * kScoreWarps;
+  for (int i = tid; i < n_big; i += kPickThreads)
+    big = fmaxf(big, p.largest[static_cast<long long>(bh) * p.n_blocks * kScoreWarps + i]);
+  for (int r = warp; r < p.rows; r += NW) {
+    const __nv_bfloat16* q = select_row(p, b, h, r);
+    float a = 0.f;
+    for (int d = lane; d < p.D; d += 32) a += fabsf(__bfloat162float(q[d]));
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) a += __shfl_xor_sync(0xffffffffu, a, d);
+    qsum = fmaxf(qsum, a);
   }
-  // listed in order: above the key, and the first `want` of those equal to it
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+  if (lane == 0) {
+    shf[warp] = big;
+    shf[NW + warp] = qsum;
+  }
+  int odd[1] = {0};  // scores that are not finite, of pages that are held
+  for (int i = tid; i < count; i += kPickThreads) {
+    const float s = score[i];
+    odd[0] += s == INFINITY;
+    if (i < kPickKeys) keys[i] = score_key(s);
+  }
+  pick_sums(odd, sh, turn);  // (a barrier: keys and shf are written)
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    big = fmaxf(big, shf[w]);
+    qsum = fmaxf(qsum, shf[NW + w]);
+  }
+  // 1 percent for the sum's and the product's own roundings; a little for
+  // products below the smallest normal number
+  const float rho = odd[0] ? INFINITY : 14.14f * 0x1p-24f * (big * qsum) + 1e-42f;
+  auto key = [&](int i) { return i < kPickKeys ? keys[i] : score_key(score[i]); };
+
+  // T, the want-th highest score: two bits a round, each the highest digit
+  // that at least `want` scores reach
+  unsigned T = 0;
+  if (want > 0) {
+    for (int shift = 30; shift >= 0; shift -= 2) {
+      int n[3] = {0, 0, 0};
+      for (int i = lo + tid; i < hi; i += kPickThreads) {
+        const unsigned k = key(i);
+#pragma unroll
+        for (int d = 0; d < 3; ++d) n[d] += k >= (T | ((d + 1u) << shift));
+      }
+      pick_sums(n, sh, turn);
+      T |= pick_digit(n, want) << shift;
+    }
+  }
+  const float t = dec_bits_float((T >> 31) ? T & 0x7fffffffu : ~T);
+  // sure: above whatever the want-th highest exact score may be; near: may
+  // be either (the comparisons with infinities and NaN fall to `near`)
+  auto value = [&](int i) {
+    const unsigned k = key(i);
+    return dec_bits_float((k >> 31) ? k & 0x7fffffffu : ~k);
+  };
+  const bool none = want == 0;
+  auto sure = [&](float s) { return !none && s - rho > t + rho; };
+  auto near = [&](float s) { return !none && !(s - rho > t + rho) && !(s + rho < t - rho); };
+  int n_of[2] = {0, 0};  // sure, near
+  for (int i = lo + tid; i < hi; i += kPickThreads) {
+    const float s = value(i);
+    n_of[0] += sure(s);
+    n_of[1] += near(s);
+  }
+  pick_sums(n_of, sh, turn);
+  want -= n_of[0];
+  const bool all_near = n_of[1] <= want;
+  unsigned long long E = 0;  // the want-th highest exact score of those near T
+  if (!all_near) {
+    for (int base = lo; base < hi; base += kPickThreads) {
+      const int i = base + warp * 32 + lane;
+      unsigned todo = dec_ballot(i < hi && near(value(i < hi ? i : lo)));
+      while (todo != 0u) {
+        const int at = base + warp * 32 + dec_lowest(todo);
+        todo &= todo - 1u;
+        const double s = exact_score(p, b, h, at);
+        if (lane == 0) exact[at] = s;
+      }
+    }
+    __syncthreads();
+    for (int shift = 62; shift >= 0; shift -= 2) {
+      int n[3] = {0, 0, 0};
+      for (int i = lo + tid; i < hi; i += kPickThreads) {
+        if (!near(value(i))) continue;
+        const unsigned long long k = score_key(exact[i]);
+#pragma unroll
+        for (int d = 0; d < 3; ++d) n[d] += k >= (E | ((d + 1ull) << shift));
+      }
+      pick_sums(n, sh, turn);
+      E |= static_cast<unsigned long long>(pick_digit(n, want)) << shift;
+    }
+    int above[1] = {0};
+    for (int i = lo + tid; i < hi; i += kPickThreads)
+      above[0] += near(value(i)) && score_key(exact[i]) > E;
+    pick_sums(above, sh, turn);
+    want -= above[0];  // places for those that equal E
+  }
+
+  // listed in order: those chosen, and the first `want` of those equal to E
   int listed = 0, equal = 0;
-  const bool none = p.n_sel == p.n_first + p.n_last;
   for (int base = 0; base < count; base += kPickThreads) {
     const int i = base + tid;
     bool take = i < count && (i < lo || i >= hi), same = false;
-    if (!none && i >= lo && i < hi) {
-      const unsigned long long k = score_key(score[i]);
-      take = k > prefix;
-      same = k == prefix;
+    if (i >= lo && i < hi) {
+      const float s = value(i);
+      take = sure(s);
+      if (near(s)) {
+        if (all_near) {
+          take = true;
+        } else {
+          const unsigned long long k = score_key(exact[i]);
+          take = k > E;
+          same = k == E;
+        }
+      }
     }
     const unsigned below = (1u << lane) - 1u;
-    const unsigned mt = dec_ballot(same);
-    if (lane == 0) sums[warp] = dec_popc(mt);
-    __syncthreads();
-    int eq = equal + dec_popc(mt & below);
-    for (int w = 0; w < kPickThreads / 32; ++w) {
-      if (w < warp) eq += sums[w];
-      equal += sums[w];
+    if (!all_near) {
+      const unsigned m = dec_ballot(same);
+      __syncthreads();
+      if (lane == 0) sh[warp] = dec_popc(m);
+      __syncthreads();
+      int eq = equal + dec_popc(m & below);
+      for (int w = 0; w < NW; ++w) {
+        if (w < warp) eq += sh[w];
+        equal += sh[w];
+      }
+      take = take || (same && eq < want);
     }
-    take = take || (same && eq < want);
-    const unsigned ml = dec_ballot(take);
-    if (lane == 0) sums[kPickThreads / 32 + warp] = dec_popc(ml);
+    const unsigned m = dec_ballot(take);
     __syncthreads();
-    int at = listed + dec_popc(ml & below);
-    for (int w = 0; w < kPickThreads / 32; ++w) {
-      if (w < warp) at += sums[kPickThreads / 32 + w];
-      listed += sums[kPickThreads / 32 + w];
+    if (lane == 0) sh[NW + warp] = dec_popc(m);
+    __syncthreads();
+    int at = listed + dec_popc(m & below);
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) at += sh[NW + w];
+      listed += sh[NW + w];
     }
     if (take && at < p.n_sel) out[at] = i;
   }
 }
 
 __host__ __device__ constexpr int pick_smem_bytes() {
-  return (258 + 2 * (kPickThreads / 32)) * 4;
+  return kPickKeys * 4 + 8 * (kPickThreads / 32) * 4;
+}
+// Workspace: the exact scores, the fp32 scores, the largest bounds.
+__host__ __device__ constexpr long long select_workspace_bytes(long long bh, int width) {
+  const long long blocks = (width + score_pages(128) - 1) / score_pages(128);
+  return bh * (width * 12LL + blocks * kScoreWarps * 4);
 }
 
 }  // namespace cattn

@@ -27,9 +27,11 @@ __device__ __forceinline__ unsigned dec_ballot(bool p) { return __ballot_sync(kF
 __device__ __forceinline__ int dec_popc(unsigned x) { return __popc(x); }
 // Index of the lowest set bit (x != 0).
 __device__ __forceinline__ int dec_lowest(unsigned x) { return __ffs(static_cast<int>(x)) - 1; }
-// atomicAdd on a shared counter.
-__device__ __forceinline__ int dec_add_shared(int* p, int v) { return atomicAdd(p, v); }
 __device__ __forceinline__ long long dec_double_bits(double x) { return __double_as_longlong(x); }
+__device__ __forceinline__ unsigned dec_float_bits(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ float dec_bits_float(unsigned u) { return __uint_as_float(u); }
+// Sum over the warp's lanes.
+__device__ __forceinline__ int dec_warp_sum(int v) { return __reduce_add_sync(kFullWarp, v); }
 // Rank of the CTA in its cluster, and the cluster's size.
 __device__ __forceinline__ unsigned dec_cluster_rank() {
   unsigned r;

@@ -200,7 +200,8 @@ static void select() {
   p.n_pages = a[5]; p.P = a[6]; p.width = a[7];
   p.n_sel = a[8]; p.n_first = a[9]; p.n_last = a[10];
   p.rows = p.H / p.Hkv * p.Tq;
-  p.n_blocks = (p.width + kScorePages - 1) / kScorePages;
+  p.D = D;
+  p.n_blocks = (p.width + score_pages(D) - 1) / score_pages(D);
   p.q = in<__nv_bfloat16>(1);
   p.q_sb = static_cast<long long>(p.H) * p.Tq * D;
   p.q_sh = static_cast<long long>(p.Tq) * D;
@@ -210,7 +211,9 @@ static void select() {
   p.table_sb = p.width;
   p.lengths = in<int>(4);
   p.pages = out<int>(static_cast<size_t>(p.B) * p.Hkv * p.n_sel);
-  p.score = out<double>(static_cast<size_t>(p.B) * p.Hkv * p.width);
+  p.exact = out<double>(static_cast<size_t>(p.B) * p.Hkv * p.width);
+  p.score = out<float>(static_cast<size_t>(p.B) * p.Hkv * p.width);
+  p.largest = out<float>(static_cast<size_t>(p.B) * p.Hkv * p.n_blocks * kScoreWarps);
   switch (D) {
     case 16: run_select<16>(p); break;
     case 32: run_select<32>(p); break;

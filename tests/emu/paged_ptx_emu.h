@@ -1,9 +1,8 @@
 // Host definitions of the paged-cache kernels' warp primitives (the functions
 // of paged_ptx.cuh), for the CPU emulator: indexed shuffles, ballots, the
-// cluster rank, counters in shared memory, bit casts.
+// cluster rank, warp sums, bit casts.
 #pragma once
 
-#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <stdexcept>
@@ -44,9 +43,22 @@ inline unsigned dec_ballot(bool p) {
 }
 inline int dec_popc(unsigned x) { return __builtin_popcount(x); }
 inline int dec_lowest(unsigned x) { return __builtin_ctz(x); }
-inline int dec_add_shared(int* p, int v) {
-  emu::check_smem(p, 4, 4);
-  return std::atomic_ref<int>(*p).fetch_add(v);
+inline unsigned dec_float_bits(float x) {
+  unsigned r;
+  std::memcpy(&r, &x, 4);
+  return r;
+}
+inline float dec_bits_float(unsigned u) {
+  float r;
+  std::memcpy(&r, &u, 4);
+  return r;
+}
+inline int dec_warp_sum(int v) {
+  const uint64_t mine = static_cast<uint64_t>(static_cast<int64_t>(v));
+  const uint64_t* all = emu::warp_exchange(&mine, 1);
+  int64_t s = 0;
+  for (int l = 0; l < 32; ++l) s += static_cast<int64_t>(all[l * emu::kWords]);
+  return static_cast<int>(s);
 }
 inline long long dec_double_bits(double x) {
   long long r;
