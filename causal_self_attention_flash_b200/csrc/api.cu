@@ -223,6 +223,27 @@ cudaError_t launch_dependent(bool dependent, void (*kernel)(KArgs...), dim3 grid
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// launch_dependent with clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), long long grid, int block, int cluster,
+                           size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 bool d_supported(int D) { return D == 16 || D == 32 || D == 64 || D == 128; }
 
 // Common shape checks. Returns CATTN_OK, or INVALID_ARG / UNSUPPORTED.
@@ -843,15 +864,21 @@ cattn_status append_impl(const AppendParams& p, cudaStream_t s) {
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 
-template <int D>
+template <int D, bool UP>
 cattn_status select_impl(const SelectParams& p, cudaStream_t s) {
   const long long bh = static_cast<long long>(p.B) * p.Hkv;
   clear_stale_error();
   LaunchTimer t(K_SELECT, s);
   cudaError_t e = cudaSuccess;
+  if (p.width > p.n_sel && select_fused(bh, p.width)) {
+    e = launch_cluster(page_select_kernel<D, UP>, bh * kSelectCtas, kSelectThreads, kSelectCtas,
+                       pick_smem_bytes(), s, p);
+    return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
+  }
   if (p.width > p.n_sel)  // (else every page is taken)
-    e = launch_dependent(true, page_score_kernel<D>, dim3(static_cast<unsigned>(bh * p.n_blocks)),
-                         dim3(kScoreThreads), 0, s, p);
+    e = launch_dependent(true, page_score_kernel<D, UP>,
+                         dim3(static_cast<unsigned>(bh * p.n_blocks)), dim3(kScoreThreads), 0, s,
+                         p);
   if (e == cudaSuccess)
     e = launch_dependent(true, page_pick_kernel, dim3(static_cast<unsigned>(bh)),
                          dim3(kPickThreads), pick_smem_bytes(), s, p);
@@ -1102,22 +1129,10 @@ cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
   long long n = (n_slots > B ? n_slots : B) / kPlanThreads + 1;
   if (n > kPlanMaxCtas) n = kPlanMaxCtas;
   clear_stale_error();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n));
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = plan_smem_bytes(B);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(n);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = n > 1 ? 2 : 1;
-  LaunchTimer t(K_CACHE, cfg.stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, p, static_cast<int>(n));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LaunchTimer t(K_CACHE, s);
+  const cudaError_t e = launch_cluster(paged_plan_kernel, n, kPlanThreads, static_cast<int>(n),
+                                       plan_smem_bytes(B), s, p, static_cast<int>(n));
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 
@@ -1148,10 +1163,12 @@ cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds
       (!workspace || workspace_bytes < attn_page_select_workspace_bytes(B, Hkv, width)))
     return CATTN_ERR_INVALID_ARG;
   SelectParams p;
-  p.n_blocks = (width + score_pages(D) - 1) / score_pages(D);
-  p.D = D;
   const long long bh = static_cast<long long>(B) * Hkv;
-  if (bh * p.n_blocks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
+  p.D = D;
+  p.groups = score_groups_of(bh, width);
+  p.n_blocks = score_blocks(bh, width);
+  if (bh * p.n_blocks > 0x7fffffffLL || bh * kSelectCtas > 0x7fffffffLL)
+    return CATTN_ERR_INVALID_ARG;
   int dev;
   if ((st = check_device(&dev)) != CATTN_OK) return st;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -1169,11 +1186,12 @@ cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds
   p.score = reinterpret_cast<float*>(p.exact + bh * width);
   p.largest = p.score + bh * width;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool up = p.rows > 8;
   switch (D) {
-    case 16: return select_impl<16>(p, s);
-    case 32: return select_impl<32>(p, s);
-    case 64: return select_impl<64>(p, s);
-    case 128: return select_impl<128>(p, s);
+    case 16: return up ? select_impl<16, true>(p, s) : select_impl<16, false>(p, s);
+    case 32: return up ? select_impl<32, true>(p, s) : select_impl<32, false>(p, s);
+    case 64: return up ? select_impl<64, true>(p, s) : select_impl<64, false>(p, s);
+    case 128: return up ? select_impl<128, true>(p, s) : select_impl<128, false>(p, s);
   }
   return CATTN_ERR_UNSUPPORTED;
 }

@@ -320,10 +320,13 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 // counts as +inf.
 //
 // The choice is that of exact sums, so that it does not depend on an order of
-// summation.  page_score_kernel sums in fp32: at most 13 roundings lie on the
-// way of a term (8 products in a lane, 5 additions between lanes), so with
-// V = the largest |bound| of the request's pages and u = 2^-24
-//   |s_i - exact| <= 14 u max_r sum_d |q_rd| V = rho.
+// summation.  page_score_kernel sums on the tensor cores (the clipped query
+// rows against the pages' bounds, 2 D terms a score): products of two bf16
+// values are exact in fp32, and each of the 2 D / 16 steps rounds sums of at
+// most S = sum of the terms' magnitudes.  Allowing a step 2^-20 S (the fp32
+// rounding is 2^-24; how the hardware aligns its addends is not documented),
+// at most 16 of them, and with V = the largest |bound| of the request's pages,
+//   |s_i - exact| <= 2^-16 max_r sum_d |q_rd| V = rho.
 // The want-th highest of a list moves by at most rho if every entry does, so
 // a page more than 2 rho above (below) the want-th highest fp32 score T is
 // chosen (is not).  Only if more pages lie within 2 rho of T than there are
@@ -341,7 +344,8 @@ struct SelectParams {
   long long table_sb;
   const int* lengths;
   int B, H, Hkv, Tq, D, rows, n_pages, P, width, n_sel, n_first, n_last;
-  int n_blocks;                 // ceil(width / score_pages(D))
+  int groups;                   // groups of 8 pages that a warp takes
+  int n_blocks;                 // CTAs per (request, head)
   int* pages;                   // (B, Hkv, n_sel)
   double* exact;                // [B Hkv][width]
   float* score;                 // [B Hkv][width]
@@ -350,14 +354,11 @@ struct SelectParams {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreLoads = 8;     // 16-byte loads of a lane in flight
-constexpr int kScoreRows = 4;      // query rows at a time
 constexpr int kPickThreads = 512;
-constexpr int kPickKeys = 8192;    // scores kept in shared memory
-
-// Pages of a warp and of a CTA: a page's bounds are 4 D bytes, D / 4 lanes.
-__host__ __device__ constexpr int score_warp_pages(int D) { return kScoreLoads * 128 / D; }
-__host__ __device__ constexpr int score_pages(int D) { return kScoreWarps * score_warp_pages(D); }
+constexpr int kSelectThreads = 256;  // of the fused kernel
+constexpr int kSelectCtas = 8;       // its cluster
+constexpr int kPickKeys = 8192;      // scores kept in shared memory
+constexpr int kPickNear = 256;       // pages near the border that fit its list
 
 __device__ __forceinline__ int select_count(const SelectParams& p, int b) {
   const int len = p.lengths[b];
@@ -372,129 +373,126 @@ __device__ __forceinline__ const __nv_bfloat16* select_row(const SelectParams& p
          t * p.q_st;
 }
 
-// Grid: B * Hkv * n_blocks.  A warp takes score_warp_pages(D) pages, all of
-// whose bounds are on their way at once; a lane holds 8 channels of lo or hi
-// of one page per load, and of up to four query rows.
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectParams p) {
-  constexpr int LP = D / 4;                 // lanes per page
-  constexpr int PW = score_warp_pages(D);
-  constexpr int NV = kScoreLoads * kScoreRows / LP;  // sums that a lane ends up with
-  constexpr int KEPT = NV > 0 ? NV : 1;
-  static_assert(kScoreLoads * kScoreRows == 32, "one sum per lane at D = 128");
+// Clipped query values: below (low) or above zero, zero instead of the
+// others; a NaN stays.
+__device__ __forceinline__ uint32_t clip_pair(uint32_t w, bool low) {
+  const float a = dec_bf16_lo(w), b = dec_bf16_hi(w);
+  const bool drop_a = low ? a > 0.f : a < 0.f, drop_b = low ? b > 0.f : b < 0.f;
+  return (drop_a ? 0u : w & 0xffffu) | (drop_b ? 0u : w & 0xffff0000u);
+}
+
+// Scores of groups of 8 pages (a warp): groups first, first + step, ...  The
+// next group's bounds are on their way while one is multiplied: lane (g, t4)
+// loads bytes 16 t4 .. + 15 of each 64-byte segment of page g's [lo | hi],
+// which are the B fragments of two k-steps (the channels of a segment enter
+// the product in the order that this gives, on both sides).  UP: more than 8
+// query rows.  Returns the largest |bound|.
+template <int D, bool UP>
+__device__ __forceinline__ float score_groups(const SelectParams& p, int b, int h, int count,
+                                              int first, int end, int step) {
+  constexpr int SEG = D / 16;         // 64-byte segments of a page's bounds
+  constexpr int NR = UP ? 2 : 1;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  float* out = p.score + (static_cast<long long>(b) * p.Hkv + h) * p.width;
+  uint32_t big2 = 0u;                 // largest |bound| of the even and odd channels
+  if (end > (count + 7) / 8) end = (count + 7) / 8;
+  auto page_of = [&](int group) {
+    const int i = group * 8 + g;
+    const int page = group < end && i < count ? p.table[b * p.table_sb + i] : -1;
+    return page < p.n_pages ? page : -1;
+  };
+  for (int r0 = 0; r0 < p.rows && first < end; r0 += 8 * NR) {
+    uint4 next[SEG];
+    int page = page_of(first), ahead = page_of(first + step);
+    auto load = [&]() {
+      const __nv_bfloat16* src =
+          p.bounds + (static_cast<long long>(page < 0 ? 0 : page) * p.Hkv + h) * 2 * D + 8 * t4;
+#pragma unroll
+      for (int s = 0; s < SEG; ++s)
+        next[s] = page < 0 ? uint4{0, 0, 0, 0} : *reinterpret_cast<const uint4*>(src + 32 * s);
+    };
+    load();
+    uint32_t qa[SEG][2][2][NR];       // [segment][k-step][half][row g, g + 8]
+#pragma unroll
+    for (int s = 0; s < SEG; ++s) {
+      const int ch = 32 * s + 8 * t4;
+      const bool low = ch < D;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        // (past the last row: the last again)
+        const int row = r0 + g + 8 * r < p.rows ? r0 + g + 8 * r : p.rows - 1;
+        const uint4 w =
+            *reinterpret_cast<const uint4*>(select_row(p, b, h, row) + (low ? ch : ch - D));
+        qa[s][0][0][r] = clip_pair(w.x, low);
+        qa[s][0][1][r] = clip_pair(w.y, low);
+        qa[s][1][0][r] = clip_pair(w.z, low);
+        qa[s][1][1][r] = clip_pair(w.w, low);
+      }
+    }
+    for (int group = first; group < end; group += step) {
+      uint4 v[SEG];
+#pragma unroll
+      for (int s = 0; s < SEG; ++s) v[s] = next[s];
+      const int held = page;          // of page g of this group
+      page = ahead;
+      ahead = page_of(group + 2 * step);
+      if (group + step < end) load();
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < SEG; ++s) {
+        dec_mma(c, qa[s][0][0][0], UP ? qa[s][0][0][NR - 1] : 0u, qa[s][0][1][0],
+                UP ? qa[s][0][1][NR - 1] : 0u, v[s].x, v[s].y);
+        dec_mma(c, qa[s][1][0][0], UP ? qa[s][1][0][NR - 1] : 0u, qa[s][1][1][0],
+                UP ? qa[s][1][1][NR - 1] : 0u, v[s].z, v[s].w);
+        if (r0 == 0) {
+          big2 = dec_bf16_absmax(big2, v[s].x);
+          big2 = dec_bf16_absmax(big2, v[s].y);
+          big2 = dec_bf16_absmax(big2, v[s].z);
+          big2 = dec_bf16_absmax(big2, v[s].w);
+        }
+      }
+      // the highest row of pages 2 t4 and 2 t4 + 1 of the group; +inf marks a
+      // sum that is not finite, which is left to the exact pass
+      float m[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        m[x] = c[x] - c[x] == 0.f ? c[x] : INFINITY;
+        if (UP) m[x] = fmaxf(m[x], c[2 + x] - c[2 + x] == 0.f ? c[2 + x] : INFINITY);
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) m[x] = fmaxf(m[x], __shfl_xor_sync(0xffffffffu, m[x], d));
+      }
+      // lanes 0 .. 7 write: lane l the group's page l, from lane l / 2 (row 0)
+      const float even = dec_shfl(m[0], (lane & 7) >> 1), odd = dec_shfl(m[1], (lane & 7) >> 1);
+      const int there = dec_shfl(held, 4 * (lane & 7)), i = group * 8 + lane;
+      if (lane < 8 && i < count) {
+        float s = there < 0 ? -INFINITY : (lane & 1) ? odd : even;
+        if (r0 > 0) s = fmaxf(s, out[i]);  // (this lane wrote it)
+        out[i] = s;
+      }
+    }
+  }
+  float big = fmaxf(dec_bf16_lo(big2), dec_bf16_hi(big2));
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+  return big;
+}
+
+// Grid: B * Hkv * n_blocks; a warp takes p.groups groups.  (No early release
+// of page_pick_kernel: its CTAs would take registers from the later waves of
+// this grid: 53.2 against 47.8 us for the two at 16 x 8 rows of 2,048 pages.)
+template <int D, bool UP>
+__global__ void __launch_bounds__(kScoreThreads, 3) page_score_kernel(const SelectParams p) {
   dec_grid_dep_wait();
-  dec_grid_dep_launch();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bh = static_cast<int>(blockIdx.x) / p.n_blocks;
   const int blk = static_cast<int>(blockIdx.x) - bh * p.n_blocks;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int count = select_count(p, b);
   if (count <= p.n_sel) return;  // every page is taken
-  const int first = blk * score_pages(D) + warp * PW;
-  if (blk * score_pages(D) >= count) return;
-  const int lp = lane % LP;           // the lane's place in its page: lo first
-  const bool low = lp < LP / 2;
-  const int ch = (lp % (LP / 2)) * 8;
-  // the warp's pages, one or more per lane; -1: not held
-  uint4 v[kScoreLoads];
-  float big = 0.f;
-  constexpr int TL = (PW + 31) / 32;
-  int pg[TL];
-#pragma unroll
-  for (int i = 0; i < TL; ++i) {
-    const int at = first + 32 * i + lane;
-    pg[i] = 32 * i + lane < PW && at < count ? p.table[b * p.table_sb + at] : -1;
-    if (pg[i] >= p.n_pages) pg[i] = -1;
-  }
-#pragma unroll
-  for (int j = 0; j < kScoreLoads; ++j) {
-    constexpr int PPL = 32 / LP;      // pages per load
-    const int i = j * PPL;            // compile-time register, lane within it
-    const int page = dec_shfl(pg[i / 32], i % 32 + lane / LP);
-    v[j] = page < 0 ? uint4{0, 0, 0, 0}
-                    : *reinterpret_cast<const uint4*>(
-                          p.bounds + ((static_cast<long long>(page) * p.Hkv + h) * 2 + !low) * D +
-                          ch);
-  }
-#pragma unroll
-  for (int j = 0; j < kScoreLoads; ++j) {
-    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      big = fmaxf(big, fmaxf(fabsf(dec_bf16_lo(w[c])), fabsf(dec_bf16_hi(w[c]))));
-  }
-  float best[KEPT];
-#pragma unroll
-  for (int i = 0; i < KEPT; ++i) best[i] = -INFINITY;
-  for (int r0 = 0; r0 < p.rows; r0 += kScoreRows) {
-    float s[kScoreLoads * kScoreRows];
-    // four rows in turn (past the last: the last again)
-#pragma unroll
-    for (int r = 0; r < kScoreRows; ++r) {
-      const uint4 qw = *reinterpret_cast<const uint4*>(
-          select_row(p, b, h, r0 + r < p.rows ? r0 + r : p.rows - 1) + ch);
-      const uint32_t w[4] = {qw.x, qw.y, qw.z, qw.w};
-      float y[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float x = (c & 1) ? dec_bf16_hi(w[c / 2]) : dec_bf16_lo(w[c / 2]);
-        y[c] = low ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);  // (a NaN stays)
-      }
-#pragma unroll
-      for (int j = 0; j < kScoreLoads; ++j) {
-        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-        float a = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          a = fmaf(y[2 * c], dec_bf16_lo(u[c]), a);
-          a = fmaf(y[2 * c + 1], dec_bf16_hi(u[c]), a);
-        }
-        s[j * kScoreRows + r] = a;
-      }
-    }
-    // sums over the LP lanes of a page: at each step a lane hands half of its
-    // values to its partner and takes the other half's, so that lane lp ends
-    // with values lp NV .. lp NV + NV - 1
-#pragma unroll
-    for (int d = LP / 2, n = kScoreLoads * kScoreRows / 2; d > 0; d /= 2, n /= 2) {
-      const bool upper = (lane & d) != 0;
-#pragma unroll
-      for (int i = 0; i < kScoreLoads * kScoreRows / 2; ++i)
-        if (i < n) {
-          const float keep = upper ? s[i + n] : s[i], give = upper ? s[i] : s[i + n];
-          s[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-        }
-    }
-    // a sum that is not finite is left to the exact pass: +inf marks it
-#pragma unroll
-    for (int i = 0; i < KEPT; ++i) best[i] = s[i] - s[i] == 0.f ? fmaxf(best[i], s[i]) : INFINITY;
-  }
-  // the highest of the four rows: values of one lane, or of 4 / NV lanes
-  constexpr int RL = KEPT < kScoreRows ? KEPT : kScoreRows;
-  float* out = p.score + static_cast<long long>(bh) * p.width;
-#pragma unroll
-  for (int i = 0; i < KEPT; i += RL) {
-    float m = best[i];
-#pragma unroll
-    for (int r = 1; r < RL; ++r) m = fmaxf(m, best[i + r]);
-#pragma unroll
-    for (int d = 1; d < kScoreRows / RL; d *= 2)
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const int value = lp * KEPT + i;  // of the lane's page group
-    const int at = (value / kScoreRows) * (32 / LP) + lane / LP;
-    // whether the page is held: from the lane that looked it up
-    int page = -1;
-#pragma unroll
-    for (int t = 0; t < TL; ++t) {
-      const int x = dec_shfl(pg[t], at % 32);
-      if (at / 32 == t) page = x;
-    }
-    if (value % kScoreRows == 0 && first + at < count) out[first + at] = page < 0 ? -INFINITY : m;
-  }
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-  if (lane == 0)
-    p.largest[(static_cast<long long>(bh) * p.n_blocks + blk) * kScoreWarps + warp] = big;
+  const int w = blk * kScoreWarps + warp;
+  const float big =
+      score_groups<D, UP>(p, b, h, count, w * p.groups, (w + 1) * p.groups, 1);
+  if (lane == 0) p.largest[static_cast<long long>(bh) * p.n_blocks * kScoreWarps + w] = big;
 }
 
 // Whole numbers in the order of the scores (both zeros alike).
@@ -507,24 +505,44 @@ __device__ __forceinline__ unsigned long long score_key(double s) {
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
-// Sums of the N values v over the CTA's threads; `sh` has two halves of three
-// words per warp, used in turn, so that one barrier is enough.
-template <int N>
-__device__ __forceinline__ void pick_sums(int (&v)[N], int* sh, int& turn) {
-  constexpr int NW = kPickThreads / 32;
-  static_assert(N <= 3 && NW <= 32, "sums");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int* half = sh + turn * 3 * NW;
+// Reductions over the NT threads of a CTA; `sh` has two halves of three words
+// per warp, used in turn, so that one barrier each is enough.
+template <int NT>
+struct PickReduce {
+  static constexpr int NW = NT / 32;
+  int* sh;
+  int turn;
+
+  template <int N>
+  __device__ __forceinline__ void sum(int (&v)[N]) {
+    static_assert(N <= 3 && NW <= 32, "words");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int* half = sh + turn * 3 * NW;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = dec_warp_sum(v[i]);
-    if (lane == 0) half[i * NW + warp] = v[i];
+    for (int i = 0; i < N; ++i) {
+      v[i] = dec_warp_sum(v[i]);
+      if (lane == 0) half[i * NW + warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = dec_warp_sum(lane < NW ? half[i * NW + lane] : 0);
+    turn ^= 1;
   }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = dec_warp_sum(lane < NW ? half[i * NW + lane] : 0);
-  turn ^= 1;
-}
+  __device__ __forceinline__ void min_max(unsigned& lo, unsigned& hi) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned* half = reinterpret_cast<unsigned*>(sh + turn * 3 * NW);
+    lo = dec_warp_min(lo);
+    hi = dec_warp_max(hi);
+    if (lane == 0) {
+      half[warp] = lo;
+      half[NW + warp] = hi;
+    }
+    __syncthreads();
+    lo = dec_warp_min(lane < NW ? half[lane] : 0xffffffffu);
+    hi = dec_warp_max(lane < NW ? half[NW + lane] : 0u);
+    turn ^= 1;
+  }
+};
 // The highest digit 0 .. 3 that at least `want` keys reach; n: how many reach
 // 1, 2 and 3.
 __device__ __forceinline__ unsigned pick_digit(const int (&n)[3], int want) {
@@ -555,32 +573,49 @@ __device__ __forceinline__ double exact_score(const SelectParams& p, int b, int 
   return best;
 }
 
-// Grid: B * Hkv CTAs of kPickThreads.
-__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
-  constexpr int NW = kPickThreads / 32;
-  dec_grid_dep_wait();
-  dec_grid_dep_launch();
+// Keys of no score (they would be NaN): a page that is chosen, and one that is
+// not.
+constexpr unsigned kKeySure = 0xffffffffu, kKeyOut = 0u;
+
+// The choice for (b, h) from its scores, by the NT threads of a CTA; `largest`:
+// n_largest maxima of the |bounds|.
+template <int NT>
+__device__ __forceinline__ void pick_pages(const SelectParams& p, int b, int h, int count,
+                                           const float* largest, int n_largest) {
+  constexpr int NW = NT / 32;
+  constexpr int KR = 2048 / NT;       // scores that a thread keeps in registers
   unsigned* keys = reinterpret_cast<unsigned*>(dec_dynamic_smem());  // [kPickKeys]
   int* sh = reinterpret_cast<int*>(keys + kPickKeys);                // [2][3][NW]
   float* shf = reinterpret_cast<float*>(sh + 6 * NW);                // [2][NW]
+  unsigned long long* sums = reinterpret_cast<unsigned long long*>(shf + 2 * NW);  // [kPickNear]
+  int* list = reinterpret_cast<int*>(sums + kPickNear);                            // [kPickNear]
+  PickReduce<NT> over{sh, 0};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bh = static_cast<int>(blockIdx.x), b = bh / p.Hkv, h = bh - b * p.Hkv;
-  const int count = select_count(p, b);
-  int* out = p.pages + static_cast<long long>(bh) * p.n_sel;
-  if (count <= p.n_sel) {
-    for (int i = tid; i < p.n_sel; i += kPickThreads) out[i] = i < count ? i : -1;
-    return;
-  }
-  const float* score = p.score + static_cast<long long>(bh) * p.width;
-  double* exact = p.exact + static_cast<long long>(bh) * p.width;
+  const long long bh = static_cast<long long>(b) * p.Hkv + h;
+  int* out = p.pages + bh * p.n_sel;
+  const float* score = p.score + bh * p.width;
+  double* exact = p.exact + bh * p.width;
   const int lo = p.n_first, hi = count - p.n_last;  // candidates: lo <= i < hi
-  int want = p.n_sel - p.n_first - p.n_last, turn = 0;
+  int want = p.n_sel - p.n_first - p.n_last;
 
   // rho: the largest |bound| and the largest sum |q| of a row
   float big = 0.f, qsum = 0.f;
-  const int n_big = (count + score_pages(p.D) - 1) / score_pages(p.D) * kScoreWarps;
-  for (int i = tid; i < n_big; i += kPickThreads)
-    big = fmaxf(big, p.largest[static_cast<long long>(bh) * p.n_blocks * kScoreWarps + i]);
+  unsigned kr[KR], lowest = 0xffffffffu, highest = 0u;
+  int odd[1] = {0};  // scores that are not finite, of pages that are held
+  auto take_in = [&](int i, float s) {
+    const unsigned k = score_key(s);
+    odd[0] += s == INFINITY;
+    if (i < kPickKeys) keys[i] = k;
+    lowest = k < lowest ? k : lowest;
+    highest = k > highest ? k : highest;
+    return k;
+  };
+#pragma unroll
+  for (int j = 0; j < KR; ++j) {
+    const int i = lo + tid + j * NT;
+    kr[j] = i < hi ? dec_float_bits(score[i]) : 0u;
+  }
+  for (int i = tid; i < n_largest; i += NT) big = fmaxf(big, largest[i]);
   for (int r = warp; r < p.rows; r += NW) {
     const __nv_bfloat16* q = select_row(p, b, h, r);
     float a = 0.f;
@@ -590,67 +625,103 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
     qsum = fmaxf(qsum, a);
   }
 #pragma unroll
+  for (int j = 0; j < KR; ++j) {
+    const int i = lo + tid + j * NT;
+    if (i < hi) kr[j] = take_in(i, dec_bits_float(kr[j]));
+  }
+  for (int i = lo + tid + KR * NT; i < hi; i += NT) take_in(i, score[i]);
+#pragma unroll
   for (int d = 1; d < 32; d *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
   if (lane == 0) {
     shf[warp] = big;
     shf[NW + warp] = qsum;
   }
-  int odd[1] = {0};  // scores that are not finite, of pages that are held
-  for (int i = tid; i < count; i += kPickThreads) {
-    const float s = score[i];
-    odd[0] += s == INFINITY;
-    if (i < kPickKeys) keys[i] = score_key(s);
-  }
-  pick_sums(odd, sh, turn);  // (a barrier: keys and shf are written)
+  over.sum(odd);  // (a barrier: keys and shf are written)
+  over.min_max(lowest, highest);
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     big = fmaxf(big, shf[w]);
     qsum = fmaxf(qsum, shf[NW + w]);
   }
   // 1 percent for the sum's and the product's own roundings; a little for
-  // products below the smallest normal number
-  const float rho = odd[0] ? INFINITY : 14.14f * 0x1p-24f * (big * qsum) + 1e-42f;
+  // terms below the smallest normal number
+  const float rho = odd[0] ? INFINITY : 1.01f * 0x1p-16f * (big * qsum) + 1e-35f;
   auto key = [&](int i) { return i < kPickKeys ? keys[i] : score_key(score[i]); };
+  auto each = [&](auto f) {  // f(page, key) of this thread's candidates
+#pragma unroll
+    for (int j = 0; j < KR; ++j)
+      if (lo + tid + j * NT < hi) f(lo + tid + j * NT, kr[j]);
+    for (int i = lo + tid + KR * NT; i < hi; i += NT) f(i, key(i));
+  };
 
-  // T, the want-th highest score: two bits a round, each the highest digit
-  // that at least `want` scores reach
-  unsigned T = 0;
+  // T, the want-th highest score: from the first bit in which the scores
+  // differ, two bits a round, each the highest digit that at least `want`
+  // scores reach; done when just `want` of them reach it
+  unsigned T = 0u;
   if (want > 0) {
-    for (int shift = 30; shift >= 0; shift -= 2) {
+    int reach = hi - lo, shift = 30;
+    while (shift > 0 && (lowest >> shift) == (highest >> shift)) shift -= 2;
+    T = shift + 2 < 32 ? highest >> (shift + 2) << (shift + 2) : 0u;
+    for (; shift >= 0 && reach != want; shift -= 2) {
       int n[3] = {0, 0, 0};
-      for (int i = lo + tid; i < hi; i += kPickThreads) {
-        const unsigned k = key(i);
+      each([&](int, unsigned k) {
 #pragma unroll
         for (int d = 0; d < 3; ++d) n[d] += k >= (T | ((d + 1u) << shift));
-      }
-      pick_sums(n, sh, turn);
-      T |= pick_digit(n, want) << shift;
+      });
+      over.sum(n);
+      const unsigned digit = pick_digit(n, want);
+      T |= digit << shift;
+      reach = digit == 0u ? reach : n[digit - 1u];
     }
+    unsigned least = 0xffffffffu, none = 0u;  // the lowest of those that reach T
+    each([&](int, unsigned k) { least = k >= T && k < least ? k : least; });
+    over.min_max(least, none);
+    T = least;
   }
-  const float t = dec_bits_float((T >> 31) ? T & 0x7fffffffu : ~T);
   // sure: above whatever the want-th highest exact score may be; near: may
   // be either (the comparisons with infinities and NaN fall to `near`)
-  auto value = [&](int i) {
-    const unsigned k = key(i);
-    return dec_bits_float((k >> 31) ? k & 0x7fffffffu : ~k);
+  auto value = [](unsigned k) { return dec_bits_float((k >> 31) ? k & 0x7fffffffu : ~k); };
+  const float t = value(T);
+  const bool some = want > 0;
+  auto sure = [&](unsigned k) { return some && value(k) - rho > t + rho; };
+  auto near = [&](unsigned k) {
+    return some && !(value(k) - rho > t + rho) && !(value(k) + rho < t - rho);
   };
-  const bool none = want == 0;
-  auto sure = [&](float s) { return !none && s - rho > t + rho; };
-  auto near = [&](float s) { return !none && !(s - rho > t + rho) && !(s + rho < t - rho); };
   int n_of[2] = {0, 0};  // sure, near
-  for (int i = lo + tid; i < hi; i += kPickThreads) {
-    const float s = value(i);
-    n_of[0] += sure(s);
-    n_of[1] += near(s);
-  }
-  pick_sums(n_of, sh, turn);
+  each([&](int, unsigned k) {
+    n_of[0] += sure(k);
+    n_of[1] += near(k);
+  });
+  over.sum(n_of);
   want -= n_of[0];
   const bool all_near = n_of[1] <= want;
+  const bool few = !all_near && n_of[1] <= kPickNear && count <= kPickKeys;
   unsigned long long E = 0;  // the want-th highest exact score of those near T
-  if (!all_near) {
-    for (int base = lo; base < hi; base += kPickThreads) {
-      const int i = base + warp * 32 + lane;
-      unsigned todo = dec_ballot(i < hi && near(value(i < hi ? i : lo)));
+  if (few) {
+    // list them, sum them, and rank each among all: the keys of those chosen
+    // become the highest, of the others the lowest
+    if (tid == 0) sh[0] = 0;
+    __syncthreads();
+    each([&](int i, unsigned k) {
+      if (near(k)) list[dec_add_shared(sh, 1)] = i;  // (in any order)
+    });
+    __syncthreads();
+    for (int j = warp; j < n_of[1]; j += NW) {
+      const double s = exact_score(p, b, h, list[j]);
+      if (lane == 0) sums[j] = score_key(s);
+    }
+    __syncthreads();
+    for (int j = tid; j < n_of[1]; j += NT) {
+      int rank = 0;
+      for (int x = 0; x < n_of[1]; ++x)
+        rank += sums[x] > sums[j] || (sums[x] == sums[j] && list[x] < list[j]);
+      keys[list[j]] = rank < want ? kKeySure : kKeyOut;
+    }
+    __syncthreads();
+  } else if (!all_near) {
+    for (int base = lo; base < hi; base += NT) {
+      const int i = base + tid;
+      unsigned todo = dec_ballot(i < hi && near(key(i < hi ? i : lo)));
       while (todo != 0u) {
         const int at = base + warp * 32 + dec_lowest(todo);
         todo &= todo - 1u;
@@ -661,42 +732,42 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
     __syncthreads();
     for (int shift = 62; shift >= 0; shift -= 2) {
       int n[3] = {0, 0, 0};
-      for (int i = lo + tid; i < hi; i += kPickThreads) {
-        if (!near(value(i))) continue;
+      each([&](int i, unsigned k32) {
+        if (!near(k32)) return;
         const unsigned long long k = score_key(exact[i]);
 #pragma unroll
         for (int d = 0; d < 3; ++d) n[d] += k >= (E | ((d + 1ull) << shift));
-      }
-      pick_sums(n, sh, turn);
+      });
+      over.sum(n);
       E |= static_cast<unsigned long long>(pick_digit(n, want)) << shift;
     }
     int above[1] = {0};
-    for (int i = lo + tid; i < hi; i += kPickThreads)
-      above[0] += near(value(i)) && score_key(exact[i]) > E;
-    pick_sums(above, sh, turn);
+    each([&](int i, unsigned k) { above[0] += near(k) && score_key(exact[i]) > E; });
+    over.sum(above);
     want -= above[0];  // places for those that equal E
   }
 
   // listed in order: those chosen, and the first `want` of those equal to E
   int listed = 0, equal = 0;
-  for (int base = 0; base < count; base += kPickThreads) {
+  for (int base = 0; base < count; base += NT) {
     const int i = base + tid;
     bool take = i < count && (i < lo || i >= hi), same = false;
     if (i >= lo && i < hi) {
-      const float s = value(i);
-      take = sure(s);
-      if (near(s)) {
-        if (all_near) {
-          take = true;
-        } else {
-          const unsigned long long k = score_key(exact[i]);
-          take = k > E;
-          same = k == E;
-        }
+      const unsigned k = key(i);
+      if (few && (k == kKeySure || k == kKeyOut)) {
+        take = k == kKeySure;
+      } else if (!near(k)) {
+        take = sure(k);
+      } else if (all_near) {
+        take = true;
+      } else {
+        const unsigned long long k64 = score_key(exact[i]);
+        take = k64 > E;
+        same = k64 == E;
       }
     }
     const unsigned below = (1u << lane) - 1u;
-    if (!all_near) {
+    if (!all_near && !few) {
       const unsigned m = dec_ballot(same);
       __syncthreads();
       if (lane == 0) sh[warp] = dec_popc(m);
@@ -721,13 +792,76 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
   }
 }
 
+// Every page of (b, h).
+__device__ __forceinline__ void pick_all(const SelectParams& p, long long bh, int count) {
+  for (int i = threadIdx.x; i < p.n_sel; i += blockDim.x)
+    p.pages[bh * p.n_sel + i] = i < count ? i : -1;
+}
+
+// Grid: B * Hkv CTAs of kPickThreads.
+__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
+  dec_grid_dep_wait();
+  dec_grid_dep_launch();
+  const int bh = static_cast<int>(blockIdx.x), b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int count = select_count(p, b);
+  if (count <= p.n_sel) {
+    pick_all(p, bh, count);
+    return;
+  }
+  pick_pages<kPickThreads>(p, b, h, count,
+                           p.largest + static_cast<long long>(bh) * p.n_blocks * kScoreWarps,
+                           p.n_blocks * kScoreWarps);
+}
+
+// Both in one launch: a cluster of kSelectCtas CTAs scores the pages of one
+// (request, head), then its first CTA chooses, while other clusters score.
+template <int D, bool UP>
+__global__ void __launch_bounds__(kSelectThreads, 2) page_select_kernel(const SelectParams p) {
+  constexpr int NW = kSelectCtas * kSelectThreads / 32;
+  dec_grid_dep_wait();
+  dec_grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bh = static_cast<int>(blockIdx.x) / kSelectCtas, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int rank = static_cast<int>(dec_cluster_rank());
+  const int count = select_count(p, b);
+  float* largest = p.largest + static_cast<long long>(bh) * NW;
+  if (count > p.n_sel) {
+    const int w = warp * kSelectCtas + rank;
+    const float big = score_groups<D, UP>(p, b, h, count, w, p.width, NW);
+    if (lane == 0) largest[w] = big;
+  }
+  dec_cluster_sync();  // every CTA's scores are written
+  if (rank != 0) return;
+  if (count <= p.n_sel)
+    pick_all(p, bh, count);
+  else
+    pick_pages<kSelectThreads>(p, b, h, count, largest, NW);
+}
+
 __host__ __device__ constexpr int pick_smem_bytes() {
-  return kPickKeys * 4 + 8 * (kPickThreads / 32) * 4;
+  return kPickKeys * 4 + 8 * (kPickThreads / 32) * 4 + kPickNear * 12;
+}
+// Whether the fused kernel is taken: where its clusters fill the GPU, or leave
+// a warp at most 4 groups of pages; fewer and longer lists need every SM.
+__host__ __device__ constexpr bool select_fused(long long bh, int width) {
+  return bh >= 148 / kSelectCtas || width <= 4 * 8 * kSelectCtas * kSelectThreads / 32;
+}
+// Otherwise: groups of 8 pages per warp (one wave of kScoreWave warps, or 4
+// groups, whose query rows then cost little), CTAs per (request, head).
+constexpr int kScoreWave = 148 * 12;
+__host__ __device__ constexpr int score_groups_of(long long bh, int width) {
+  const long long n = bh * ((width + 7LL) / 8) / kScoreWave;
+  return n < 1 ? 1 : n > 4 ? 4 : static_cast<int>(n);
+}
+__host__ __device__ constexpr int score_blocks(long long bh, int width) {
+  const int pages = kScoreWarps * 8 * score_groups_of(bh, width);
+  return (width + pages - 1) / pages;
 }
 // Workspace: the exact scores, the fp32 scores, the largest bounds.
 __host__ __device__ constexpr long long select_workspace_bytes(long long bh, int width) {
-  const long long blocks = (width + score_pages(128) - 1) / score_pages(128);
-  return bh * (width * 12LL + blocks * kScoreWarps * 4);
+  const long long n = select_fused(bh, width) ? kSelectCtas * kSelectThreads / 32
+                                              : score_blocks(bh, width) * kScoreWarps;
+  return bh * (width * 12LL + n * 4);
 }
 
 }  // namespace cattn

@@ -32,11 +32,24 @@ __device__ __forceinline__ unsigned dec_float_bits(float x) { return __float_as_
 __device__ __forceinline__ float dec_bits_float(unsigned u) { return __uint_as_float(u); }
 // Sum over the warp's lanes.
 __device__ __forceinline__ int dec_warp_sum(int v) { return __reduce_add_sync(kFullWarp, v); }
+__device__ __forceinline__ unsigned dec_warp_min(unsigned v) {
+  return __reduce_min_sync(kFullWarp, v);
+}
+__device__ __forceinline__ unsigned dec_warp_max(unsigned v) {
+  return __reduce_max_sync(kFullWarp, v);
+}
+// atomicAdd on a shared counter.
+__device__ __forceinline__ int dec_add_shared(int* p, int v) { return atomicAdd(p, v); }
 // Rank of the CTA in its cluster, and the cluster's size.
 __device__ __forceinline__ unsigned dec_cluster_rank() {
   unsigned r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
   return r;
+}
+// Per bf16 half: max(m, |x|), m >= 0 (the bit patterns of magnitudes are in
+// their order).
+__device__ __forceinline__ uint32_t dec_bf16_absmax(uint32_t m, uint32_t x) {
+  return __vmaxu2(m, x & 0x7fff7fffu);
 }
 // bf16 halves of a word as floats (exact).
 __device__ __forceinline__ float dec_bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -182,15 +182,20 @@ static void append() {
   put(p.bounds, g_bytes[6]);
 }
 
-template <int D>
-static void run_select(const SelectParams& p) {
+template <int D, bool UP>
+static void run_select(const SelectParams& p, bool fused) {
   const auto bh = static_cast<unsigned>(p.B * p.Hkv);
-  if (p.width > p.n_sel)
-    emu::launch_ex(bh * p.n_blocks, kScoreThreads, 0, 1, page_score_kernel<D>, p);
+  if (fused) {
+    emu::launch_ex(bh * kSelectCtas, kSelectThreads, pick_smem_bytes(), kSelectCtas,
+                   page_select_kernel<D, UP>, p);
+    return;
+  }
+  emu::launch_ex(bh * p.n_blocks, kScoreThreads, 0, 1, page_score_kernel<D, UP>, p);
   emu::launch_ex(bh, kPickThreads, pick_smem_bytes(), 1, page_pick_kernel, p);
 }
 
-// params: B H Hkv Tq D n_pages P width n_sel n_first n_last
+// params: B H Hkv Tq D n_pages P width n_sel n_first n_last groups (0: the
+//         fused kernel)
 // arrays: q, bounds, table, lengths
 static void select() {
   const int64_t* a = in<int64_t>(0);
@@ -201,7 +206,10 @@ static void select() {
   p.n_sel = a[8]; p.n_first = a[9]; p.n_last = a[10];
   p.rows = p.H / p.Hkv * p.Tq;
   p.D = D;
-  p.n_blocks = (p.width + score_pages(D) - 1) / score_pages(D);
+  const bool fused = a[11] == 0;
+  p.groups = fused ? 1 : a[11];
+  const int per = kScoreWarps * 8 * p.groups;
+  p.n_blocks = (p.width + per - 1) / per;
   p.q = in<__nv_bfloat16>(1);
   p.q_sb = static_cast<long long>(p.H) * p.Tq * D;
   p.q_sh = static_cast<long long>(p.Tq) * D;
@@ -213,12 +221,14 @@ static void select() {
   p.pages = out<int>(static_cast<size_t>(p.B) * p.Hkv * p.n_sel);
   p.exact = out<double>(static_cast<size_t>(p.B) * p.Hkv * p.width);
   p.score = out<float>(static_cast<size_t>(p.B) * p.Hkv * p.width);
-  p.largest = out<float>(static_cast<size_t>(p.B) * p.Hkv * p.n_blocks * kScoreWarps);
+  p.largest = out<float>(static_cast<size_t>(p.B) * p.Hkv * (fused ? kSelectCtas * kSelectThreads / 32
+                                                                    : p.n_blocks * kScoreWarps));
+  const bool up = p.rows > 8;
   switch (D) {
-    case 16: run_select<16>(p); break;
-    case 32: run_select<32>(p); break;
-    case 64: run_select<64>(p); break;
-    case 128: run_select<128>(p); break;
+    case 16: up ? run_select<16, true>(p, fused) : run_select<16, false>(p, fused); break;
+    case 32: up ? run_select<32, true>(p, fused) : run_select<32, false>(p, fused); break;
+    case 64: up ? run_select<64, true>(p, fused) : run_select<64, false>(p, fused); break;
+    case 128: up ? run_select<128, true>(p, fused) : run_select<128, false>(p, fused); break;
     default: std::exit(4);
   }
   put(p.pages, 4ull * p.B * p.Hkv * p.n_sel);

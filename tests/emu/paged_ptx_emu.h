@@ -3,6 +3,7 @@
 // cluster rank, warp sums, bit casts.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <stdexcept>
@@ -60,12 +61,30 @@ inline int dec_warp_sum(int v) {
   for (int l = 0; l < 32; ++l) s += static_cast<int64_t>(all[l * emu::kWords]);
   return static_cast<int>(s);
 }
+inline unsigned dec_warp_min(unsigned v) {
+  const uint64_t mine = v;
+  const uint64_t* all = emu::warp_exchange(&mine, 1);
+  uint64_t r = all[0];
+  for (int l = 1; l < 32; ++l) r = all[l * emu::kWords] < r ? all[l * emu::kWords] : r;
+  return static_cast<unsigned>(r);
+}
+inline unsigned dec_warp_max(unsigned v) { return ~dec_warp_min(~v); }
+inline int dec_add_shared(int* p, int v) {
+  emu::check_smem(p, 4, 4);
+  return std::atomic_ref<int>(*p).fetch_add(v);
+}
 inline long long dec_double_bits(double x) {
   long long r;
   std::memcpy(&r, &x, 8);
   return r;
 }
 inline unsigned dec_cluster_rank() { return emu::t_cta->rank; }
+inline uint32_t dec_bf16_absmax(uint32_t m, uint32_t x) {
+  x &= 0x7fff7fffu;
+  const uint32_t lo = (m & 0xffffu) > (x & 0xffffu) ? m & 0xffffu : x & 0xffffu;
+  const uint32_t hi = (m >> 16) > (x >> 16) ? m >> 16 : x >> 16;
+  return lo | hi << 16;
+}
 inline float dec_bf16_lo(uint32_t w) {
   const uint32_t u = w << 16;
   float f;

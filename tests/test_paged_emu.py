@@ -307,7 +307,7 @@ def test_append_nan_keys_and_odd_pages(emu):
 # ----------------------------------------------------------------- select
 
 def run_select(emu, lengths, Hkv, G, Tq, D, P, K, n_first=1, n_last=1, spare=0, holes=(),
-               change=None, seed=0):
+               change=None, seed=0, groups=0):
     B, H = len(lengths), Hkv * G
     width = max(opaged.n_pages_of(n, P) for n in lengths) + spare
     n_pages = sum(opaged.n_pages_of(n, P) for n in lengths) + 2
@@ -320,7 +320,8 @@ def run_select(emu, lengths, Hkv, G, Tq, D, P, K, n_first=1, n_last=1, spare=0, 
     q = rows(seed + 3, B, H, Tq, D)
     if change:
         change(q, bounds, table)
-    raw = emu("select", [B, H, Hkv, Tq, D, n_pages, P, width, K, n_first, n_last], bits(q),
+    raw = emu("select", [B, H, Hkv, Tq, D, n_pages, P, width, K, n_first, n_last,
+                         groups], bits(q),
               bits(bounds), table, np.array(lengths, np.int32))
     got = np.frombuffer(raw, np.int32).reshape(B, Hkv, K)
     want = opaged.select(as64(q), as64(bounds), table, lengths, P, K, n_first, n_last)
@@ -332,10 +333,12 @@ def run_select(emu, lengths, Hkv, G, Tq, D, P, K, n_first=1, n_last=1, spare=0, 
     ([900], 2, 3, 1, 128, 8, 20, 0, 0),
     ([700, 640], 1, 2, 4, 32, 16, 8, 2, 3),
     ([333], 1, 1, 2, 16, 3, 2, 1, 1),          # nothing but the first and the last
+    ([500], 1, 5, 4, 64, 8, 9, 1, 1),          # 20 rows: two tiles of 16
     ([1200], 1, 1, 1, 16, 4, 290, 1, 1),       # all but a few; more pages than threads
 ])
 def test_select(emu, lengths, Hkv, G, Tq, D, P, K, n_first, n_last):
     run_select(emu, lengths, Hkv, G, Tq, D, P, K, n_first, n_last, spare=3)
+    run_select(emu, lengths, Hkv, G, Tq, D, P, K, n_first, n_last, seed=20, groups=3)
 
 
 def test_select_ties_nan_and_pages_that_are_not_held(emu):
