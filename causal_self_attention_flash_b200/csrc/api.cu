@@ -865,20 +865,23 @@ cattn_status append_impl(const AppendParams& p, cudaStream_t s) {
 }
 
 template <int D, bool UP>
-cattn_status select_impl(const SelectParams& p, cudaStream_t s) {
+cattn_status select_impl(const SelectParams& p, int dev, cudaStream_t s) {
   const long long bh = static_cast<long long>(p.B) * p.Hkv;
   clear_stale_error();
   LaunchTimer t(K_SELECT, s);
   cudaError_t e = cudaSuccess;
   if (p.width > p.n_sel && select_fused(bh, p.width)) {
+    const cattn_status st = ensure_smem(dev, 77 + 2 * d_index(D) + UP, page_select_kernel<D, UP>,
+                                        select_smem_bytes(D));
+    if (st != CATTN_OK) return st;
     e = launch_cluster(page_select_kernel<D, UP>, bh * kSelectCtas, kSelectThreads, kSelectCtas,
-                       pick_smem_bytes(), s, p);
+                       select_smem_bytes(D), s, p);
     return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
   }
   if (p.width > p.n_sel)  // (else every page is taken)
     e = launch_dependent(true, page_score_kernel<D, UP>,
-                         dim3(static_cast<unsigned>(bh * p.n_blocks)), dim3(kScoreThreads), 0, s,
-                         p);
+                         dim3(static_cast<unsigned>(bh * p.n_blocks)), dim3(kScoreThreads),
+                         kScoreWarps * score_ring_bytes(D), s, p);
   if (e == cudaSuccess)
     e = launch_dependent(true, page_pick_kernel, dim3(static_cast<unsigned>(bh)),
                          dim3(kPickThreads), pick_smem_bytes(), s, p);
@@ -1188,10 +1191,10 @@ cattn_status attn_page_select(const void* q, cattn_layout lq, const void* bounds
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool up = p.rows > 8;
   switch (D) {
-    case 16: return up ? select_impl<16, true>(p, s) : select_impl<16, false>(p, s);
-    case 32: return up ? select_impl<32, true>(p, s) : select_impl<32, false>(p, s);
-    case 64: return up ? select_impl<64, true>(p, s) : select_impl<64, false>(p, s);
-    case 128: return up ? select_impl<128, true>(p, s) : select_impl<128, false>(p, s);
+    case 16: return up ? select_impl<16, true>(p, dev, s) : select_impl<16, false>(p, dev, s);
+    case 32: return up ? select_impl<32, true>(p, dev, s) : select_impl<32, false>(p, dev, s);
+    case 64: return up ? select_impl<64, true>(p, dev, s) : select_impl<64, false>(p, dev, s);
+    case 128: return up ? select_impl<128, true>(p, dev, s) : select_impl<128, false>(p, dev, s);
   }
   return CATTN_ERR_UNSUPPORTED;
 }

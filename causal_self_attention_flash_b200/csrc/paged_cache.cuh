@@ -354,6 +354,7 @@ struct SelectParams {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreStages = 3;      // groups of 8 pages in flight per warp
 constexpr int kPickThreads = 512;
 constexpr int kSelectThreads = 256;  // of the fused kernel
 constexpr int kSelectCtas = 8;       // its cluster
@@ -381,38 +382,66 @@ __device__ __forceinline__ uint32_t clip_pair(uint32_t w, bool low) {
   return (drop_a ? 0u : w & 0xffffu) | (drop_b ? 0u : w & 0xffff0000u);
 }
 
-// Scores of groups of 8 pages (a warp): groups first, first + step, ...  The
-// next group's bounds are on their way while one is multiplied: lane (g, t4)
-// loads bytes 16 t4 .. + 15 of each 64-byte segment of page g's [lo | hi],
-// which are the B fragments of two k-steps (the channels of a segment enter
-// the product in the order that this gives, on both sides).  UP: more than 8
-// query rows.  Returns the largest |bound|.
+__host__ __device__ constexpr int score_ring_bytes(int D) { return kScoreStages * 32 * D; }
+
+// Scores of groups of 8 pages (a warp): groups first, first + step, ... below
+// `end`.  Their bounds stream through the warp's ring of kScoreStages slots of
+// 32 D bytes with cp.async; lane (g, t4) reads bytes 16 t4 .. + 15 of each
+// 64-byte segment of page g's [lo | hi], which are the B fragments of two
+// k-steps (the channels of a segment enter the product in the order that this
+// gives, on both sides).  The page numbers of four groups are looked up at a
+// time, one per lane, ahead of their use.  UP: more than 8 query rows.
+// Returns the largest |bound|.
 template <int D, bool UP>
 __device__ __forceinline__ float score_groups(const SelectParams& p, int b, int h, int count,
-                                              int first, int end, int step) {
+                                              int first, int end, int step, uint8_t* ring) {
   constexpr int SEG = D / 16;         // 64-byte segments of a page's bounds
+  constexpr int PCS = D / 4;          // its 16-byte pieces
   constexpr int NR = UP ? 2 : 1;
   const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   float* out = p.score + (static_cast<long long>(b) * p.Hkv + h) * p.width;
+  const __nv_bfloat16* src = p.bounds + static_cast<long long>(h) * 2 * D;
+  const long long page_step = static_cast<long long>(p.Hkv) * 2 * D;
   uint32_t big2 = 0u;                 // largest |bound| of the even and odd channels
   if (end > (count + 7) / 8) end = (count + 7) / 8;
-  auto page_of = [&](int group) {
-    const int i = group * 8 + g;
-    const int page = group < end && i < count ? p.table[b * p.table_sb + i] : -1;
-    return page < p.n_pages ? page : -1;
+  // pages at odd places take the other 64 bytes of each 128: two pages' reads
+  // then fall into different banks
+  auto at = [](int page, int pc) {
+    return page * (4 * D) + (pc ^ (PCS >= 8 ? (page & 1) * 4 : 0)) * 16;
   };
   for (int r0 = 0; r0 < p.rows && first < end; r0 += 8 * NR) {
-    uint4 next[SEG];
-    int page = page_of(first), ahead = page_of(first + step);
-    auto load = [&]() {
-      const __nv_bfloat16* src =
-          p.bounds + (static_cast<long long>(page < 0 ? 0 : page) * p.Hkv + h) * 2 * D + 8 * t4;
-#pragma unroll
-      for (int s = 0; s < SEG; ++s)
-        next[s] = page < 0 ? uint4{0, 0, 0, 0} : *reinterpret_cast<const uint4*>(src + 32 * s);
-    };
-    load();
+    const int n = (end - first + step - 1) / step;
     uint32_t qa[SEG][2][2][NR];       // [segment][k-step][half][row g, g + 8]
+    // lane l looks up page l % 8 of group l / 8 of four
+    auto look_up = [&](int k4) {
+      const int i = (first + (4 * k4 + (lane >> 3)) * step) * 8 + (lane & 7);
+      const int page = 4 * k4 + (lane >> 3) < n && i < count ? p.table[b * p.table_sb + i] : -1;
+      return page < p.n_pages ? page : -1;
+    };
+    int now = look_up(0), then = look_up(1), have = 0;  // entries of have, have + 1
+    uint32_t held = 0u;               // which pages of the groups in the ring are held, 8 bits each
+    auto issue = [&](int k) {         // group k of the run into slot k % kScoreStages
+      held <<= 8;
+      if (k < n) {
+        if (k / 4 != have) {
+          have = k / 4;
+          now = then;
+          then = look_up(have + 1);
+        }
+        held |= (dec_ballot(now >= 0) >> ((k & 3) * 8)) & 0xffu;
+        uint8_t* to = ring + (k % kScoreStages) * (32 * D);
+#pragma unroll
+        for (int u = 0; u < PCS / 4; ++u) {
+          const int piece = lane + 32 * u, pg = piece / PCS, pc = piece % PCS;
+          const int page = dec_shfl(now, (k & 3) * 8 + pg);
+          const bool ok = page >= 0;
+          dec_cp_async16(to + at(pg, pc), src + (ok ? page : 0) * page_step + pc * 8, ok);
+        }
+      }
+      dec_cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kScoreStages; ++k) issue(k);
 #pragma unroll
     for (int s = 0; s < SEG; ++s) {
       const int ch = 32 * s + 8 * t4;
@@ -429,28 +458,28 @@ __device__ __forceinline__ float score_groups(const SelectParams& p, int b, int 
         qa[s][1][1][r] = clip_pair(w.w, low);
       }
     }
-    for (int group = first; group < end; group += step) {
-      uint4 v[SEG];
-#pragma unroll
-      for (int s = 0; s < SEG; ++s) v[s] = next[s];
-      const int held = page;          // of page g of this group
-      page = ahead;
-      ahead = page_of(group + 2 * step);
-      if (group + step < end) load();
+    for (int k = 0; k < n; ++k) {
+      dec_cp_async_wait<kScoreStages - 1>();
+      __syncwarp();  // every lane's pieces of the group are in shared memory
+      const uint8_t* slot = ring + (k % kScoreStages) * (32 * D);
       float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < SEG; ++s) {
+        const uint4 v = *reinterpret_cast<const uint4*>(slot + at(g, 4 * s + t4));
         dec_mma(c, qa[s][0][0][0], UP ? qa[s][0][0][NR - 1] : 0u, qa[s][0][1][0],
-                UP ? qa[s][0][1][NR - 1] : 0u, v[s].x, v[s].y);
+                UP ? qa[s][0][1][NR - 1] : 0u, v.x, v.y);
         dec_mma(c, qa[s][1][0][0], UP ? qa[s][1][0][NR - 1] : 0u, qa[s][1][1][0],
-                UP ? qa[s][1][1][NR - 1] : 0u, v[s].z, v[s].w);
+                UP ? qa[s][1][1][NR - 1] : 0u, v.z, v.w);
         if (r0 == 0) {
-          big2 = dec_bf16_absmax(big2, v[s].x);
-          big2 = dec_bf16_absmax(big2, v[s].y);
-          big2 = dec_bf16_absmax(big2, v[s].z);
-          big2 = dec_bf16_absmax(big2, v[s].w);
+          big2 = dec_bf16_absmax(big2, v.x);
+          big2 = dec_bf16_absmax(big2, v.y);
+          big2 = dec_bf16_absmax(big2, v.z);
+          big2 = dec_bf16_absmax(big2, v.w);
         }
       }
+      const uint32_t there = held >> (8 * (kScoreStages - 1));
+      __syncwarp();  // every lane has read the slot: refill it
+      issue(k + kScoreStages);
       // the highest row of pages 2 t4 and 2 t4 + 1 of the group; +inf marks a
       // sum that is not finite, which is left to the exact pass
       float m[2];
@@ -463,13 +492,14 @@ __device__ __forceinline__ float score_groups(const SelectParams& p, int b, int 
       }
       // lanes 0 .. 7 write: lane l the group's page l, from lane l / 2 (row 0)
       const float even = dec_shfl(m[0], (lane & 7) >> 1), odd = dec_shfl(m[1], (lane & 7) >> 1);
-      const int there = dec_shfl(held, 4 * (lane & 7)), i = group * 8 + lane;
+      const int i = (first + k * step) * 8 + lane;
       if (lane < 8 && i < count) {
-        float s = there < 0 ? -INFINITY : (lane & 1) ? odd : even;
+        float s = ((there >> lane) & 1u) == 0u ? -INFINITY : (lane & 1) ? odd : even;
         if (r0 > 0) s = fmaxf(s, out[i]);  // (this lane wrote it)
         out[i] = s;
       }
     }
+    dec_cp_async_wait<0>();
   }
   float big = fmaxf(dec_bf16_lo(big2), dec_bf16_hi(big2));
 #pragma unroll
@@ -479,9 +509,9 @@ __device__ __forceinline__ float score_groups(const SelectParams& p, int b, int 
 
 // Grid: B * Hkv * n_blocks; a warp takes p.groups groups.  (No early release
 // of page_pick_kernel: its CTAs would take registers from the later waves of
-// this grid: 53.2 against 47.8 us for the two at 16 x 8 rows of 2,048 pages.)
+// this grid, 5 us of 48 when it was measured at 128 x 1,150 pages.)
 template <int D, bool UP>
-__global__ void __launch_bounds__(kScoreThreads, 3) page_score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 4) page_score_kernel(const SelectParams p) {
   dec_grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bh = static_cast<int>(blockIdx.x) / p.n_blocks;
@@ -490,8 +520,8 @@ __global__ void __launch_bounds__(kScoreThreads, 3) page_score_kernel(const Sele
   const int count = select_count(p, b);
   if (count <= p.n_sel) return;  // every page is taken
   const int w = blk * kScoreWarps + warp;
-  const float big =
-      score_groups<D, UP>(p, b, h, count, w * p.groups, (w + 1) * p.groups, 1);
+  const float big = score_groups<D, UP>(p, b, h, count, w * p.groups, (w + 1) * p.groups, 1,
+                                        dec_dynamic_smem() + warp * score_ring_bytes(D));
   if (lane == 0) p.largest[static_cast<long long>(bh) * p.n_blocks * kScoreWarps + w] = big;
 }
 
@@ -827,7 +857,8 @@ __global__ void __launch_bounds__(kSelectThreads, 2) page_select_kernel(const Se
   float* largest = p.largest + static_cast<long long>(bh) * NW;
   if (count > p.n_sel) {
     const int w = warp * kSelectCtas + rank;
-    const float big = score_groups<D, UP>(p, b, h, count, w, p.width, NW);
+    const float big = score_groups<D, UP>(p, b, h, count, w, p.width, NW,
+                                          dec_dynamic_smem() + warp * score_ring_bytes(D));
     if (lane == 0) largest[w] = big;
   }
   dec_cluster_sync();  // every CTA's scores are written
@@ -841,17 +872,27 @@ __global__ void __launch_bounds__(kSelectThreads, 2) page_select_kernel(const Se
 __host__ __device__ constexpr int pick_smem_bytes() {
   return kPickKeys * 4 + 8 * (kPickThreads / 32) * 4 + kPickNear * 12;
 }
-// Whether the fused kernel is taken: where its clusters fill the GPU, or leave
-// a warp at most 4 groups of pages; fewer and longer lists need every SM.
-__host__ __device__ constexpr bool select_fused(long long bh, int width) {
-  return bh >= 148 / kSelectCtas || width <= 4 * 8 * kSelectCtas * kSelectThreads / 32;
+// Shared memory of the fused kernel: the rings, and then the choice's.
+__host__ __device__ constexpr int select_smem_bytes(int D) {
+  const int rings = kSelectThreads / 32 * score_ring_bytes(D);
+  return rings > pick_smem_bytes() ? rings : pick_smem_bytes();
 }
-// Otherwise: groups of 8 pages per warp (one wave of kScoreWave warps, or 4
-// groups, whose query rows then cost little), CTAs per (request, head).
-constexpr int kScoreWave = 148 * 12;
+
+// Whether the fused kernel is taken: for short lists, where it saves a launch
+// (device time is the same: 16 heads x 512 pages 11.6 against 11.9 us, x 1,024
+// pages 14.2 against 14.1); longer ones are scored faster by a grid of its
+// own (64 x 256 pages: 13.9 against 17.9 us, 128 x 1,150: 33.2 against 45.6).
+__host__ __device__ constexpr bool select_fused(long long bh, int width) {
+  return bh * ((width + 7LL) / 8) <= 2048;
+}
+// Otherwise: groups of 8 pages per warp, and the CTAs per (request, head) that
+// follow.  One group where there are few, so that all are on their way at
+// once; up to six, whose query rows then cost little (64 x 512 pages: 17.2 us
+// with one, 15.5 with two; 32 x 2,048: 27.4, 22.7 with four; 128 x 1,150:
+// 47.0, 33.2 with six).
 __host__ __device__ constexpr int score_groups_of(long long bh, int width) {
-  const long long n = bh * ((width + 7LL) / 8) / kScoreWave;
-  return n < 1 ? 1 : n > 4 ? 4 : static_cast<int>(n);
+  const long long n = (bh * ((width + 7LL) / 8) + 2047) / 2048;
+  return n < 1 ? 1 : n > 6 ? 6 : static_cast<int>(n);
 }
 __host__ __device__ constexpr int score_blocks(long long bh, int width) {
   const int pages = kScoreWarps * 8 * score_groups_of(bh, width);

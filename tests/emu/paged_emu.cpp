@@ -186,11 +186,12 @@ template <int D, bool UP>
 static void run_select(const SelectParams& p, bool fused) {
   const auto bh = static_cast<unsigned>(p.B * p.Hkv);
   if (fused) {
-    emu::launch_ex(bh * kSelectCtas, kSelectThreads, pick_smem_bytes(), kSelectCtas,
+    emu::launch_ex(bh * kSelectCtas, kSelectThreads, select_smem_bytes(D), kSelectCtas,
                    page_select_kernel<D, UP>, p);
     return;
   }
-  emu::launch_ex(bh * p.n_blocks, kScoreThreads, 0, 1, page_score_kernel<D, UP>, p);
+  emu::launch_ex(bh * p.n_blocks, kScoreThreads, kScoreWarps * score_ring_bytes(D), 1,
+                 page_score_kernel<D, UP>, p);
   emu::launch_ex(bh, kPickThreads, pick_smem_bytes(), 1, page_pick_kernel, p);
 }
 
