@@ -853,14 +853,18 @@ cattn_status paged_decode(const void* q, cattn_layout lq, const void* k, cattn_l
 
 template <int D>
 cattn_status append_impl(const AppendParams& p, cudaStream_t s) {
-  const long long blocks = (p.n * p.Hkv * (D / 8) + kAppendThreads - 1) / kAppendThreads;
+  const int tile = append_tile(p.n);
+  const long long blocks = p.bounds
+                               ? (p.n + tile - 1) / tile
+                               : (p.n * p.Hkv * (D / 8) + kAppendThreads - 1) / kAppendThreads;
   if (blocks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
   clear_stale_error();
   LaunchTimer t(K_CACHE, s);
-  const dim3 g(static_cast<unsigned>(blocks));
+  const dim3 g(static_cast<unsigned>(blocks)), b(kAppendThreads);
   const cudaError_t e =
-      p.bounds ? launch_dependent(true, cache_append_kernel<D, true>, g, dim3(kAppendThreads), 0, s, p)
-               : launch_dependent(true, cache_append_kernel<D, false>, g, dim3(kAppendThreads), 0, s, p);
+      p.bounds ? launch_dependent(true, cache_append_bounds_kernel<D>, g, b, append_smem_bytes(),
+                                  s, p, tile)
+               : launch_dependent(true, cache_append_kernel<D>, g, b, 0, s, p);
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 
@@ -1049,7 +1053,7 @@ cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, const void* 
                                void* stream) {
   cattn_status st = check_paged(1, Hkv, Hkv, D, n_pages, page_size, 1);
   if (st != CATTN_OK) return st;
-  if (n < 0) return CATTN_ERR_INVALID_ARG;
+  if (n < 0 || n > (1LL << 40)) return CATTN_ERR_INVALID_ARG;
   if (n == 0) return CATTN_OK;
   if (!k_new || !v_new || !slots || !k_cache || !v_cache) return CATTN_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8) || !aligned(k_cache, 16) ||
@@ -1128,14 +1132,12 @@ cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
   p.slots = reinterpret_cast<long long*>(slots);
   p.positions = positions;
   p.status = status;
-  // a CTA per kPlanThreads slots or requests, as far as one cluster goes
-  long long n = (n_slots > B ? n_slots : B) / kPlanThreads + 1;
-  if (n > kPlanMaxCtas) n = kPlanMaxCtas;
+  const int n = plan_ctas(n_slots, B);
   clear_stale_error();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   LaunchTimer t(K_CACHE, s);
-  const cudaError_t e = launch_cluster(paged_plan_kernel, n, kPlanThreads, static_cast<int>(n),
-                                       plan_smem_bytes(B), s, p, static_cast<int>(n));
+  const cudaError_t e = launch_cluster(paged_plan_kernel, n, plan_threads(n_slots, B), n,
+                                       plan_smem_bytes(B), s, p, n);
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 

@@ -28,7 +28,7 @@ namespace cattn {
 // the first write of the outputs (which may be the same arrays), and then the
 // CTAs share the tokens and pages.
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 1024;    // at most; 256 for short calls
 constexpr int kPlanMaxB = 8192;       // requests per call (128 KB of prefix sums)
 constexpr int kPlanMaxCtas = 8;       // portable cluster size
 constexpr int kPlanStatusInvalid = 1;   // CATTN_ERR_INVALID_ARG
@@ -52,7 +52,7 @@ struct PlanParams {
 };
 
 __host__ __device__ constexpr int plan_smem_bytes(int B) {
-  return 16 * (B + 1) + kPlanThreads / 32 * 32 + 16;
+  return 16 * (B + 1) + kPlanThreads / 32 * 32 + 16;  // prefix sums, warp totals, faults
 }
 
 __device__ __forceinline__ int pages_of(int n, int P) { return n / P + (n % P != 0); }
@@ -76,25 +76,36 @@ __device__ __forceinline__ long long warp_scan64(long long v, int lane) {
   return v;
 }
 
-// Grid: one cluster of n_ctas <= kPlanMaxCtas CTAs of kPlanThreads threads.
+// CTAs of a call (its cluster) and their threads: one CTA where it holds a slot
+// and a request per thread.
+__host__ __device__ constexpr int plan_threads(long long n_slots, int B) {
+  return n_slots <= 1024 && B <= 256 ? 256 : kPlanThreads;
+}
+__host__ __device__ constexpr int plan_ctas(long long n_slots, int B) {
+  const long long n = (n_slots + kPlanThreads - 1) / kPlanThreads;
+  (void)B;
+  return n < 1 ? 1 : n > kPlanMaxCtas ? kPlanMaxCtas : static_cast<int>(n);
+}
+
+// Grid: one cluster of n_ctas CTAs.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p, int n_ctas) {
   dec_grid_dep_wait();
   dec_grid_dep_launch();
-  constexpr int NW = kPlanThreads / 32;
   uint8_t* smem = dec_dynamic_smem();
-  long long* sums = reinterpret_cast<long long*>(smem);  // [NW][3], then the flag
-  int* bad = reinterpret_cast<int*>(sums + NW * 4);
+  long long* sums = reinterpret_cast<long long*>(smem);  // [warps][4]
+  int* bad = reinterpret_cast<int*>(sums + kPlanThreads / 32 * 4);
   int* len_s = bad + 4;                                   // [B + 1] each
   int* cu_tok = len_s + p.B + 1;
   int* cu_need = cu_tok + p.B + 1;
   int* cu_back = cu_need + p.B + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nt = static_cast<int>(blockDim.x), nw = nt / 32;
   const unsigned rank = n_ctas > 1 ? dec_cluster_rank() : 0u;
   if (tid < 4) bad[tid] = 0;
   __syncthreads();
 
   // this thread's requests: b0 .. b1 - 1
-  const int nb = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int nb = (p.B + nt - 1) / nt;
   const int b0 = tid * nb < p.B ? tid * nb : p.B, b1 = b0 + nb < p.B ? b0 + nb : p.B;
   const int cap = p.width * p.P;
   long long tok = 0, need = 0, back = 0;
@@ -124,18 +135,17 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     sums[warp * 4 + 2] = ib;
   }
   __syncthreads();
-  long long et = it - tok, en = in - need, eb = ib - back, T = 0, N = 0, R = 0;
+  // the warps' totals, scanned by every warp
+  long long of[3], all[3];
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) {
-      et += sums[w * 4];
-      en += sums[w * 4 + 1];
-      eb += sums[w * 4 + 2];
-    }
-    T += sums[w * 4];
-    N += sums[w * 4 + 1];
-    R += sums[w * 4 + 2];
+  for (int i = 0; i < 3; ++i) {
+    const long long v = warp_scan64(lane < nw ? sums[lane * 4 + i] : 0, lane);
+    all[i] = dec_shfl(v, 31);
+    of[i] = dec_shfl(v, warp > 0 ? warp - 1 : 0);
+    if (warp == 0) of[i] = 0;
   }
+  long long et = of[0] + it - tok, en = of[1] + in - need, eb = of[2] + ib - back;
+  long long T = all[0], N = all[1], R = all[2];
   const long long head = p.state[0], tail = p.state[1], avail = tail - head;
   int status = 0;
   if (T > p.n_slots || N > avail) status = kPlanStatusTooLarge;
@@ -163,27 +173,41 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   __syncthreads();
   if (n_ctas > 1) dec_cluster_sync();  // every CTA has read its inputs
 
-  const int start = static_cast<int>(rank) * kPlanThreads + tid, step = n_ctas * kPlanThreads;
+  const int start = static_cast<int>(rank) * nt + tid, step = n_ctas * nt;
   const int head0 = static_cast<int>(head % p.n_pages >= 0 ? head % p.n_pages : 0);
   const int tail0 = static_cast<int>(tail % p.n_pages >= 0 ? tail % p.n_pages : 0);
   auto at = [&](int base, int k) {  // ring entry of counter base + k, k < n_pages
     const long long i = static_cast<long long>(base) + k;
     return static_cast<int>(i >= p.n_pages ? i - p.n_pages : i);
   };
-  for (long long i = start; i < p.n_slots; i += step) {
-    long long slot = -1;
-    int pos = -1;
-    if (i < T) {
-      const int b = last_at_most(cu_tok, p.B, static_cast<int>(i));
-      const int len = len_s[b], have = pages_of(len, p.P);
-      pos = len + (static_cast<int>(i) - cu_tok[b]);
-      const int lp = pos / p.P;
-      const int page = lp < have ? p.table[b * p.table_sb + lp]
-                                 : p.ring[at(head0, cu_need[b] + lp - have)];
-      if (page >= 0 && page < p.n_pages) slot = static_cast<long long>(page) * p.P + pos % p.P;
+  // four tokens at a time: their searches and look-ups overlap
+  constexpr int ILP = 4;
+  for (long long i0 = start; i0 < p.n_slots; i0 += ILP * step) {
+    int page[ILP], pos[ILP], row[ILP];
+#pragma unroll
+    for (int u = 0; u < ILP; ++u) {
+      const long long i = i0 + static_cast<long long>(u) * step;
+      page[u] = pos[u] = -1;
+      row[u] = 0;
+      if (i < T) {
+        const int b = last_at_most(cu_tok, p.B, static_cast<int>(i));
+        const int len = len_s[b], have = pages_of(len, p.P);
+        pos[u] = len + (static_cast<int>(i) - cu_tok[b]);
+        const int lp = pos[u] / p.P;
+        row[u] = pos[u] - lp * p.P;
+        page[u] = lp < have ? p.table[b * p.table_sb + lp]
+                            : p.ring[at(head0, cu_need[b] + lp - have)];
+      }
     }
-    p.slots[i] = slot;
-    p.positions[i] = pos;
+#pragma unroll
+    for (int u = 0; u < ILP; ++u) {
+      const long long i = i0 + static_cast<long long>(u) * step;
+      if (i >= p.n_slots) continue;
+      p.slots[i] = page[u] >= 0 && page[u] < p.n_pages
+                       ? static_cast<long long>(page[u]) * p.P + row[u]
+                       : -1;
+      p.positions[i] = pos[u];
+    }
   }
   for (int j = start; j < N; j += step) {
     const int b = last_at_most(cu_need, p.B, j);
@@ -232,21 +256,19 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendILP = 8;         // rows of a run in flight per thread
+constexpr int kAppendMaxTile = 32;    // tokens per CTA, a lane each
 
-// min / max of bf16 values that keep a NaN
-__device__ __forceinline__ float min_nan(float a, float b) {
-  return a != a ? a : b != b ? b : fminf(a, b);
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  return a != a ? a : b != b ? b : fmaxf(a, b);
+// Tokens per CTA of the form with bounds: about 512 CTAs.
+__host__ __device__ constexpr int append_tile(long long n) {
+  return n < 1024 ? 1 : n / 512 > kAppendMaxTile ? kAppendMaxTile : static_cast<int>(n / 512);
 }
 
-// Thread: 8 channels of one (row, head).
-template <int D, bool BOUNDS>
+// Without bounds.  Thread: 8 channels of one (row, head).
+template <int D>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
   constexpr int PC = D / 8;
   dec_grid_dep_wait();
-  dec_grid_dep_launch();
   const long long x = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x;
   const int pc = static_cast<int>(x % PC);
   const long long unit = x / PC;
@@ -255,56 +277,120 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
   if (i >= p.n) return;
   const long long slot = p.slots[i];
   if (slot < 0 || slot >= p.n_rows) return;
-  const long long page = slot / p.P;
-  int off = static_cast<int>(slot - page * p.P);
-  if (BOUNDS && off != 0 && i > 0 && p.slots[i - 1] == slot - 1) return;  // inside a run
-  const bool fresh = off == 0;
-  float lo[8], hi[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    lo[c] = INFINITY;
-    hi[c] = -INFINITY;
-  }
-  const __nv_bfloat16* ks = p.kn + i * p.kn_st + h * p.kn_sh + pc * 8;
-  const __nv_bfloat16* vs = p.vn + i * p.vn_st + h * p.vn_sh + pc * 8;
-  __nv_bfloat16* kd = p.k + page * p.k_sp + h * p.k_sh + pc * 8;
-  __nv_bfloat16* vd = p.v + page * p.v_sp + h * p.v_sh + pc * 8;
-  for (long long j = i;; ++j, ++off) {
-    const uint4 kw = *reinterpret_cast<const uint4*>(ks + (j - i) * p.kn_st);
-    const uint4 vw = *reinterpret_cast<const uint4*>(vs + (j - i) * p.vn_st);
-    *reinterpret_cast<uint4*>(kd + off * p.k_st) = kw;
-    *reinterpret_cast<uint4*>(vd + off * p.v_st) = vw;
-    if (!BOUNDS) return;
-    const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float a = dec_bf16_lo(w[c]), b = dec_bf16_hi(w[c]);
-      lo[2 * c] = min_nan(lo[2 * c], a);
-      hi[2 * c] = max_nan(hi[2 * c], a);
-      lo[2 * c + 1] = min_nan(lo[2 * c + 1], b);
-      hi[2 * c + 1] = max_nan(hi[2 * c + 1], b);
-    }
-    if (off + 1 >= p.P || j + 1 >= p.n || p.slots[j + 1] != slot + (j + 1 - i)) break;
-  }
-  uint4* bl = reinterpret_cast<uint4*>(p.bounds + ((page * p.Hkv + h) * 2) * D + pc * 8);
-  uint4* bh = reinterpret_cast<uint4*>(p.bounds + ((page * p.Hkv + h) * 2 + 1) * D + pc * 8);
-  if (!fresh) {
-    const uint4 a = *bl, b = *bh;
-    const uint32_t wl[4] = {a.x, a.y, a.z, a.w}, wh[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      lo[2 * c] = min_nan(lo[2 * c], dec_bf16_lo(wl[c]));
-      lo[2 * c + 1] = min_nan(lo[2 * c + 1], dec_bf16_hi(wl[c]));
-      hi[2 * c] = max_nan(hi[2 * c], dec_bf16_lo(wh[c]));
-      hi[2 * c + 1] = max_nan(hi[2 * c + 1], dec_bf16_hi(wh[c]));
-    }
-  }
-  // (the values are bf16 values: packing them rounds nothing)
-  *bl = uint4{dec_pack_bf16(lo[0], lo[1]), dec_pack_bf16(lo[2], lo[3]),
-              dec_pack_bf16(lo[4], lo[5]), dec_pack_bf16(lo[6], lo[7])};
-  *bh = uint4{dec_pack_bf16(hi[0], hi[1]), dec_pack_bf16(hi[2], hi[3]),
-              dec_pack_bf16(hi[4], hi[5]), dec_pack_bf16(hi[6], hi[7])};
+  const long long page = slot / p.P, off = slot - page * p.P;
+  const uint4 k =
+      *reinterpret_cast<const uint4*>(p.kn + i * p.kn_st + h * p.kn_sh + pc * 8);
+  const uint4 v =
+      *reinterpret_cast<const uint4*>(p.vn + i * p.vn_st + h * p.vn_sh + pc * 8);
+  *reinterpret_cast<uint4*>(p.k + page * p.k_sp + h * p.k_sh + off * p.k_st + pc * 8) = k;
+  *reinterpret_cast<uint4*>(p.v + page * p.v_sp + h * p.v_sh + off * p.v_st + pc * 8) = v;
 }
+
+// With bounds.  Grid: ceil(n / tile) CTAs; a CTA takes the runs that begin
+// among its `tile` tokens, to their ends.  Unit: 8 channels of K or of V of
+// one head of a run; its thread reads kAppendILP rows at a time.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads)
+    cache_append_bounds_kernel(const AppendParams p, int tile) {
+  constexpr int PC = D / 8;
+  dec_grid_dep_wait();
+  uint8_t* smem = dec_dynamic_smem();
+  long long* run_slot = reinterpret_cast<long long*>(smem);            // [32]
+  int* run_at = reinterpret_cast<int*>(run_slot + kAppendMaxTile);     // [32]
+  int* run_len = run_at + kAppendMaxTile;                              // [32]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long i0 = static_cast<long long>(blockIdx.x) * tile;
+  auto valid = [&](long long slot) { return slot >= 0 && slot < p.n_rows; };
+  // token j goes on with the run of token j - 1
+  auto goes_on = [&](long long j) {
+    if (j <= 0 || j >= p.n) return false;
+    const long long slot = p.slots[j];
+    return valid(slot) && p.slots[j - 1] == slot - 1 && slot % p.P != 0;
+  };
+  const bool in = lane < tile && i0 + lane < p.n;
+  const long long slot = in ? p.slots[i0 + lane] : -1;
+  const bool on = in && goes_on(i0 + lane);
+  const unsigned stops = ~dec_ballot(on);                     // no run goes on there
+  const unsigned leads = dec_ballot(valid(slot) && !on);
+  const int n_runs = dec_popc(leads);
+  if (n_runs == 0) return;
+  if (warp == 0) {
+    // a run ends before the next stop of the tile, or is followed beyond it
+    const unsigned inside = tile < 32 ? (1u << tile) - 1u : ~0u;
+    const unsigned behind = lane < 31 ? stops & inside & (~0u << (lane + 1)) : 0u;
+    int len = behind != 0u ? dec_lowest(behind) - lane : tile - lane;
+    const bool open = ((leads >> lane) & 1u) != 0u && behind == 0u;
+    if (dec_ballot(open) != 0u) {
+      long long j = i0 + tile;
+      for (;; j += 32) {
+        const unsigned end = ~dec_ballot(goes_on(j + lane));
+        if (end != 0u) {
+          j += dec_lowest(end);
+          break;
+        }
+      }
+      if (open) len = static_cast<int>(j - (i0 + lane));
+    }
+    if ((leads >> lane) & 1u) {
+      const int r = dec_popc(leads & ((1u << lane) - 1u));
+      run_slot[r] = slot;
+      run_at[r] = lane;
+      run_len[r] = len;
+    }
+  }
+  __syncthreads();
+  const int per_run = 2 * p.Hkv * PC;
+  for (int u = tid; u < n_runs * per_run; u += kAppendThreads) {
+    const int r = u / per_run, rest = u - r * per_run;
+    const bool keys = rest < p.Hkv * PC;
+    const int hp = keys ? rest : rest - p.Hkv * PC, h = hp / PC, pc = hp - h * PC;
+    const long long first = run_slot[r], page = first / p.P, i = i0 + run_at[r];
+    const int off = static_cast<int>(first - page * p.P), n = run_len[r];
+    const long long from_st = keys ? p.kn_st : p.vn_st, to_st = keys ? p.k_st : p.v_st;
+    const __nv_bfloat16* from = keys ? p.kn + i * p.kn_st + h * p.kn_sh + pc * 8
+                                     : p.vn + i * p.vn_st + h * p.vn_sh + pc * 8;
+    __nv_bfloat16* to = keys ? p.k + page * p.k_sp + h * p.k_sh + off * p.k_st + pc * 8
+                             : p.v + page * p.v_sp + h * p.v_sh + off * p.v_st + pc * 8;
+    uint4* bl = reinterpret_cast<uint4*>(p.bounds + ((page * p.Hkv + h) * 2) * D + pc * 8);
+    uint4 lo, hi;
+    if (keys) {
+      if (off != 0) {  // the page goes on
+        lo = *bl;
+        hi = bl[D / 8];
+      } else {
+        lo = hi = *reinterpret_cast<const uint4*>(from);
+      }
+    }
+    for (int t = 0; t < n; t += kAppendILP) {
+      uint4 x[kAppendILP];
+#pragma unroll
+      for (int j = 0; j < kAppendILP; ++j)  // (past the last: the last again)
+        x[j] = *reinterpret_cast<const uint4*>(from + (t + j < n ? t + j : n - 1) * from_st);
+#pragma unroll
+      for (int j = 0; j < kAppendILP; ++j)
+        if (t + j < n) *reinterpret_cast<uint4*>(to + (t + j) * to_st) = x[j];
+      if (keys) {
+#pragma unroll
+        for (int j = 0; j < kAppendILP; ++j) {
+          lo.x = dec_bf16_min(lo.x, x[j].x);
+          lo.y = dec_bf16_min(lo.y, x[j].y);
+          lo.z = dec_bf16_min(lo.z, x[j].z);
+          lo.w = dec_bf16_min(lo.w, x[j].w);
+          hi.x = dec_bf16_max(hi.x, x[j].x);
+          hi.y = dec_bf16_max(hi.y, x[j].y);
+          hi.z = dec_bf16_max(hi.z, x[j].z);
+          hi.w = dec_bf16_max(hi.w, x[j].w);
+        }
+      }
+    }
+    if (keys) {
+      *bl = lo;
+      bl[D / 8] = hi;
+    }
+  }
+}
+
+__host__ __device__ constexpr int append_smem_bytes() { return kAppendMaxTile * 16; }
 
 // ------------------------------------------------------------------ select
 //

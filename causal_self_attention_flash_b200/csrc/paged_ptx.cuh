@@ -51,6 +51,17 @@ __device__ __forceinline__ unsigned dec_cluster_rank() {
 __device__ __forceinline__ uint32_t dec_bf16_absmax(uint32_t m, uint32_t x) {
   return __vmaxu2(m, x & 0x7fff7fffu);
 }
+// Per bf16 half, the lower and the higher value; a NaN stays.
+__device__ __forceinline__ uint32_t dec_bf16_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t dec_bf16_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // bf16 halves of a word as floats (exact).
 __device__ __forceinline__ float dec_bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float dec_bf16_hi(uint32_t w) {

@@ -108,7 +108,7 @@ static void decode() {
   put(p.lse, rows * 4);
 }
 
-// params: B width n_pages P n_slots ctas in_place
+// params: B width n_pages P n_slots ctas in_place threads
 // arrays: asked, lengths, table, ring, state
 static void plan() {
   const int64_t* a = in<int64_t>(0);
@@ -128,7 +128,7 @@ static void plan() {
   p.slots = out<long long>(p.n_slots);
   p.positions = out<int>(p.n_slots);
   p.status = out<int>(1);
-  emu::launch_ex(ctas, kPlanThreads, plan_smem_bytes(p.B), ctas, paged_plan_kernel, p,
+  emu::launch_ex(ctas, a[7], plan_smem_bytes(p.B), ctas, paged_plan_kernel, p,
                  static_cast<int>(ctas));
   put(p.lengths_out, 4ull * p.B);
   put(p.state_out, 16);
@@ -141,16 +141,18 @@ static void plan() {
 }
 
 template <int D>
-static void run_append(const AppendParams& p) {
+static void run_append(const AppendParams& p, int tile) {
+  if (p.bounds) {
+    emu::launch_ex(static_cast<unsigned>((p.n + tile - 1) / tile), kAppendThreads,
+                   append_smem_bytes(), 1, cache_append_bounds_kernel<D>, p, tile);
+    return;
+  }
   const auto blocks =
       static_cast<unsigned>((p.n * p.Hkv * (D / 8) + kAppendThreads - 1) / kAppendThreads);
-  if (p.bounds)
-    emu::launch_ex(blocks, kAppendThreads, 0, 1, cache_append_kernel<D, true>, p);
-  else
-    emu::launch_ex(blocks, kAppendThreads, 0, 1, cache_append_kernel<D, false>, p);
+  emu::launch_ex(blocks, kAppendThreads, 0, 1, cache_append_kernel<D>, p);
 }
 
-// params: n Hkv D n_pages P; arrays: k_new, v_new (n, Hkv, D), slots, k, v
+// params: n Hkv D n_pages P tile; arrays: k_new, v_new (n, Hkv, D), slots, k, v
 // (n_pages, P, Hkv, D), bounds
 static void append() {
   const int64_t* a = in<int64_t>(0);
@@ -171,10 +173,10 @@ static void append() {
   p.k_sh = p.v_sh = D;
   p.k_st = p.v_st = static_cast<long long>(p.Hkv) * D;
   switch (D) {
-    case 16: run_append<16>(p); break;
-    case 32: run_append<32>(p); break;
-    case 64: run_append<64>(p); break;
-    case 128: run_append<128>(p); break;
+    case 16: run_append<16>(p, a[5]); break;
+    case 32: run_append<32>(p, a[5]); break;
+    case 64: run_append<64>(p, a[5]); break;
+    case 128: run_append<128>(p, a[5]); break;
     default: std::exit(4);
   }
   put(p.k, g_bytes[4]);

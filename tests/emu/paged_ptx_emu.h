@@ -97,5 +97,26 @@ inline float dec_bf16_hi(uint32_t w) {
   std::memcpy(&f, &u, 4);
   return f;
 }
+namespace emu_detail {
+template <typename F>
+inline uint32_t per_half(uint32_t a, uint32_t b, F f) {
+  uint32_t r = 0;
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t ha = half ? a & 0xffff0000u : a << 16, hb = half ? b & 0xffff0000u : b << 16;
+    float x, y;
+    std::memcpy(&x, &ha, 4);
+    std::memcpy(&y, &hb, 4);
+    const uint32_t h = x != x || y != y ? 0x7fffu : (f(x, y) ? ha : hb) >> 16;
+    r |= h << (16 * half);
+  }
+  return r;
+}
+}  // namespace emu_detail
+inline uint32_t dec_bf16_min(uint32_t a, uint32_t b) {
+  return emu_detail::per_half(a, b, [](float x, float y) { return x <= y; });
+}
+inline uint32_t dec_bf16_max(uint32_t a, uint32_t b) {
+  return emu_detail::per_half(a, b, [](float x, float y) { return x >= y; });
+}
 
 }  // namespace cattn

@@ -186,9 +186,10 @@ def test_sparse(emu, Tq, G):
 
 # ------------------------------------------------------------------- plan
 
-def run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas=1, in_place=False):
+def run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas=1, in_place=False,
+             threads=256):
     B, width = table.shape
-    raw = emu("plan", [B, width, len(ring), P, n_slots, ctas, int(in_place)],
+    raw = emu("plan", [B, width, len(ring), P, n_slots, ctas, int(in_place), threads],
               np.array(asked, np.int32), np.array(lengths, np.int32), table.astype(np.int32),
               np.array(ring, np.int32), np.array(state, np.int64))
     got = take(raw, (np.int32, B), (np.int64, 2), (np.int32, B + 1), (np.int64, n_slots),
@@ -218,14 +219,14 @@ def plan_inputs(seed, B, P, longest, most, spare=4):
     return asked, lengths, table, ring, np.array([head, head + len(free)])
 
 
-@pytest.mark.parametrize("B,P,longest,most,ctas", [
-    (1, 16, 40, 1, 1), (5, 16, 100, 30, 1), (40, 8, 60, 3, 2), (9, 5, 33, 200, 2),
-    (300, 16, 64, 1, 2), (7, 1, 9, 4, 1)])
+@pytest.mark.parametrize("B,P,longest,most,ctas,threads", [
+    (1, 16, 40, 1, 1, 256), (5, 16, 100, 30, 1, 256), (40, 8, 60, 3, 2, 256),
+    (9, 5, 33, 200, 2, 256), (300, 16, 64, 1, 2, 64), (7, 1, 9, 4, 1, 1024)])
 @pytest.mark.parametrize("in_place", [False, True])
-def test_plan(emu, B, P, longest, most, ctas, in_place):
+def test_plan(emu, B, P, longest, most, ctas, threads, in_place):
     asked, lengths, table, ring, state = plan_inputs(B + P, B, P, longest, most)
     n_slots = int(np.maximum(asked, 0).sum()) + 3
-    want = run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas, in_place)
+    want = run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas, in_place, threads)
     assert want["status"] == opaged.OK
 
 
@@ -268,7 +269,7 @@ def test_plan_without_requests_and_with_foreign_pages(emu):
 
 # ----------------------------------------------------------------- append
 
-def run_append(emu, slots, Hkv, D, n_pages, P, bounds=True, bad=None, seed=0):
+def run_append(emu, slots, Hkv, D, n_pages, P, bounds=True, bad=None, seed=0, tile=1):
     n = len(slots)
     kn, vn = rows(seed + 1, n, Hkv, D), rows(seed + 2, n, Hkv, D)
     if bad is not None:
@@ -276,7 +277,7 @@ def run_append(emu, slots, Hkv, D, n_pages, P, bounds=True, bad=None, seed=0):
     k, v = rows(seed + 3, n_pages, Hkv, P, D), rows(seed + 4, n_pages, Hkv, P, D)
     lo = rows(seed + 5, n_pages, Hkv, 1, D)
     bd = torch.cat([lo, lo + 1], 2)
-    raw = emu("append", [n, Hkv, D, n_pages, P], bits(kn), bits(vn), np.array(slots, np.int64),
+    raw = emu("append", [n, Hkv, D, n_pages, P, tile], bits(kn), bits(vn), np.array(slots, np.int64),
               bits(k.transpose(1, 2)), bits(v.transpose(1, 2)),
               bits(bd) if bounds else np.zeros(0, np.int16))
     size = k.numel()
@@ -296,12 +297,17 @@ def test_append(emu, D, bounds):
     # a run inside a page, a page boundary, skipped and foreign slots, lone rows
     slots = [21, 22, 23, 24, 25, 40, -1, 3, 10 ** 12, 8, 9, 50, 55, -2 ** 62]
     run_append(emu, slots, 3, D, 8, 8, bounds)
+    run_append(emu, slots, 3, D, 8, 8, bounds, tile=4)
+    run_append(emu, slots, 3, D, 8, 8, bounds, tile=32)
 
 
 def test_append_nan_keys_and_odd_pages(emu):
     run_append(emu, [3, 4, 5, 6, 7, 12], 1, 64, 4, 5, bad=2)
     run_append(emu, [0], 1, 16, 1, 1)
-    run_append(emu, list(range(7, 40)), 2, 64, 3, 20)
+    for tile in (1, 5, 32):
+        run_append(emu, list(range(7, 60)), 2, 64, 3, 20, tile=tile)
+    run_append(emu, list(range(3, 120)), 1, 16, 1, 130, tile=3)     # one run over many tiles
+    run_append(emu, [5, 5 + 2 ** 40, 6, 7], 1, 16, 1, 16, tile=4)   # a run that breaks off
 
 
 # ----------------------------------------------------------------- select
