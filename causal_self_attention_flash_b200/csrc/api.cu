@@ -1115,8 +1115,10 @@ cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
     return CATTN_ERR_INVALID_ARG;
   int dev;
   if ((st = check_device(&dev)) != CATTN_OK) return st;
-  if ((st = ensure_smem(dev, 76, paged_plan_kernel, plan_smem_bytes(kPlanMaxB))) != CATTN_OK)
-    return st;
+  const bool prompts = plan_prompts(n_slots);
+  const auto kernel = prompts ? paged_plan_kernel<false> : paged_plan_kernel<true>;
+  st = ensure_smem(dev, 85 + prompts, kernel, plan_smem_bytes(kPlanMaxB));
+  if (st != CATTN_OK) return st;
   PlanParams p;
   p.asked = new_tokens;
   p.lengths = lengths;
@@ -1132,12 +1134,19 @@ cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
   p.slots = reinterpret_cast<long long*>(slots);
   p.positions = positions;
   p.status = status;
+  plan_divider(p);
   const int n = plan_ctas(n_slots, B);
   clear_stale_error();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   LaunchTimer t(K_CACHE, s);
-  const cudaError_t e = launch_cluster(paged_plan_kernel, n, plan_threads(n_slots, B), n,
-                                       plan_smem_bytes(B), s, p, n);
+  cudaError_t e =
+      launch_cluster(kernel, n, plan_threads(n_slots, B), n, plan_smem_bytes(B), s, p, n);
+  if (e == cudaSuccess && prompts) {
+    const long long per = kSlotsV * kSlotsThreads;
+    e = launch_dependent(true, paged_slots_kernel,
+                         dim3(static_cast<unsigned>((n_slots + per - 1) / per)),
+                         dim3(kSlotsThreads), 0, s, p);
+  }
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 

@@ -22,8 +22,8 @@ namespace cattn {
 // ring[tail + sum have ..].  A call that cannot be served as a whole
 // changes nothing but its status.
 //
-// A few kilobytes of whole numbers: bound by latency.  One launch of one
-// thread-block cluster: every CTA scans all requests for itself (into shared
+// A few kilobytes of whole numbers: bound by latency.  One thread-block
+// cluster: every CTA scans all requests for itself (into shared
 // memory), the cluster's barrier separates the last read of the inputs from
 // the first write of the outputs (which may be the same arrays), and then the
 // CTAs share the tokens and pages.
@@ -49,7 +49,21 @@ struct PlanParams {
   long long* slots;            // (n_slots)
   int* positions;              // (n_slots)
   int* status;                 // (1)
+  // n / P for 0 <= n <= 2^30 as (n mul) >> shift: with shift = 31 + L, 2^L >= P,
+  // and mul = floor(2^shift / P) + 1 <= 2^32, n mul / 2^shift exceeds n / P by at most
+  // n / 2^shift <= 1 / (2 P), too little to reach the next whole number.
+  unsigned long long mul;
+  int shift;
+  __host__ __device__ int by_P(int n) const {
+    return static_cast<int>((static_cast<unsigned long long>(n) * mul) >> shift);
+  }
 };
+__host__ __device__ inline void plan_divider(PlanParams& p) {
+  int L = 0;
+  while ((1LL << L) < p.P) ++L;
+  p.shift = 31 + L;
+  p.mul = (1ull << p.shift) / static_cast<unsigned>(p.P) + 1;
+}
 
 __host__ __device__ constexpr int plan_smem_bytes(int B) {
   return 16 * (B + 1) + kPlanThreads / 32 * 32 + 16;  // prefix sums, warp totals, faults
@@ -57,9 +71,8 @@ __host__ __device__ constexpr int plan_smem_bytes(int B) {
 
 __device__ __forceinline__ int pages_of(int n, int P) { return n / P + (n % P != 0); }
 
-// Last index b in [0, n) with cu[b] <= i (cu ascending, cu[0] = 0 <= i).
-__device__ __forceinline__ int last_at_most(const int* cu, int n, int i) {
-  int lo = 0, hi = n;
+// Last index b in [lo, hi) with cu[b] <= i (cu ascending, cu[lo] <= i).
+__device__ __forceinline__ int last_at_most(const int* cu, int lo, int hi, int i) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (cu[mid] <= i) lo = mid; else hi = mid;
@@ -76,18 +89,26 @@ __device__ __forceinline__ long long warp_scan64(long long v, int lane) {
   return v;
 }
 
-// CTAs of a call (its cluster) and their threads: one CTA where it holds a slot
-// and a request per thread.
+// Many tokens (prompts) get a second launch over the whole GPU: the eight SMs of
+// a cluster store no more than 0.3 TB/s (145,000 slots: 20.7 us in one launch).
+__host__ __device__ constexpr bool plan_prompts(long long n_slots) {
+  return n_slots > 2 * kPlanMaxCtas * kPlanThreads;
+}
+// CTAs of the cluster and their threads: short calls on one small CTA (64
+// requests, one token each: 3.1 us); else what the slots, or the pages that
+// change hands, can occupy.
 __host__ __device__ constexpr int plan_threads(long long n_slots, int B) {
-  return n_slots <= 1024 && B <= 256 ? 256 : kPlanThreads;
+  return n_slots <= 512 && B <= 256 ? 256 : kPlanThreads;
 }
 __host__ __device__ constexpr int plan_ctas(long long n_slots, int B) {
-  const long long n = (n_slots + kPlanThreads - 1) / kPlanThreads;
-  (void)B;
+  const long long pages = n_slots / 16 + 2LL * B, work = plan_prompts(n_slots) ? 0 : n_slots;
+  const long long n = ((work > pages ? work : pages) + kPlanThreads - 1) / kPlanThreads;
   return n < 1 ? 1 : n > kPlanMaxCtas ? kPlanMaxCtas : static_cast<int>(n);
 }
 
-// Grid: one cluster of n_ctas CTAs.
+// Grid: one cluster of n_ctas CTAs.  SLOTS: with the tokens' slots and positions
+// (else paged_slots_kernel writes them).
+template <bool SLOTS>
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p, int n_ctas) {
   dec_grid_dep_wait();
   dec_grid_dep_launch();
@@ -108,6 +129,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   const int nb = (p.B + nt - 1) / nt;
   const int b0 = tid * nb < p.B ? tid * nb : p.B, b1 = b0 + nb < p.B ? b0 + nb : p.B;
   const int cap = p.width * p.P;
+  auto pages = [&](int n) {  // n <= 2^30
+    const int q = p.by_P(n);
+    return q + (n != q * p.P);
+  };
   long long tok = 0, need = 0, back = 0;
   int fault = 0;  // bit 0: invalid, bit 1: too large
   for (int b = b0; b < b1; ++b) {
@@ -119,10 +144,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
         fault |= 2;
       } else {
         tok += n;
-        need += pages_of(len + n, p.P) - pages_of(len, p.P);
+        need += pages(len + n) - pages(len);
       }
     } else if (n < 0) {
-      if (len > cap) fault |= 1; else back += pages_of(len, p.P);
+      if (len > cap) fault |= 1; else back += pages(len);
     }
   }
   if (fault & 1) bad[1] = 1;  // (any writer writes the same)
@@ -160,9 +185,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     cu_back[b] = status ? 0 : static_cast<int>(eb);
     if (!status && n > 0) {
       et += n;
-      en += pages_of(len + n, p.P) - pages_of(len, p.P);
+      en += pages(len + n) - pages(len);
     }
-    if (!status && n < 0) eb += pages_of(len, p.P);
+    if (!status && n < 0) eb += pages(len);
   }
   if (status) T = N = R = 0;
   if (tid == 0) {
@@ -180,42 +205,57 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     const long long i = static_cast<long long>(base) + k;
     return static_cast<int>(i >= p.n_pages ? i - p.n_pages : i);
   };
-  // four tokens at a time: their searches and look-ups overlap
+  // a token per thread: its request by a search, its page from the row or, if
+  // it is new, from the ring
+  for (long long i = start; SLOTS && i < p.n_slots; i += step) {
+    long long slot = -1;
+    int pos = -1;
+    if (i < T) {
+      const int b = last_at_most(cu_tok, 0, p.B, static_cast<int>(i));
+      const int have = pages(len_s[b]);
+      pos = len_s[b] + (static_cast<int>(i) - cu_tok[b]);
+      const int lp = p.by_P(pos);
+      const int page = lp < have ? p.table[b * p.table_sb + lp]
+                                 : p.ring[at(head0, cu_need[b] + lp - have)];
+      if (page >= 0 && page < p.n_pages)
+        slot = static_cast<long long>(page) * p.P + (pos - lp * p.P);
+    }
+    p.slots[i] = slot;
+    p.positions[i] = pos;
+  }
+  // new pages into the table, freed ones into the ring, four at a time
   constexpr int ILP = 4;
-  for (long long i0 = start; i0 < p.n_slots; i0 += ILP * step) {
-    int page[ILP], pos[ILP], row[ILP];
+  for (int j0 = start; j0 < N; j0 += ILP * step) {
+    int entry[ILP];
 #pragma unroll
     for (int u = 0; u < ILP; ++u) {
-      const long long i = i0 + static_cast<long long>(u) * step;
-      page[u] = pos[u] = -1;
-      row[u] = 0;
-      if (i < T) {
-        const int b = last_at_most(cu_tok, p.B, static_cast<int>(i));
-        const int len = len_s[b], have = pages_of(len, p.P);
-        pos[u] = len + (static_cast<int>(i) - cu_tok[b]);
-        const int lp = pos[u] / p.P;
-        row[u] = pos[u] - lp * p.P;
-        page[u] = lp < have ? p.table[b * p.table_sb + lp]
-                            : p.ring[at(head0, cu_need[b] + lp - have)];
+      const long long j = j0 + static_cast<long long>(u) * step;
+      entry[u] = j < N ? p.ring[at(head0, static_cast<int>(j))] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < ILP; ++u) {
+      const long long j = j0 + static_cast<long long>(u) * step;
+      if (j >= N) continue;
+      const int b = last_at_most(cu_need, 0, p.B, static_cast<int>(j));
+      p.table[b * p.table_sb + pages(len_s[b]) + (j - cu_need[b])] = entry[u];
+    }
+  }
+  for (int j0 = start; j0 < R; j0 += ILP * step) {
+    int entry[ILP];
+#pragma unroll
+    for (int u = 0; u < ILP; ++u) {
+      const long long j = j0 + static_cast<long long>(u) * step;
+      entry[u] = -1;
+      if (j < R) {
+        const int b = last_at_most(cu_back, 0, p.B, static_cast<int>(j));
+        entry[u] = p.table[b * p.table_sb + (j - cu_back[b])];
       }
     }
 #pragma unroll
     for (int u = 0; u < ILP; ++u) {
-      const long long i = i0 + static_cast<long long>(u) * step;
-      if (i >= p.n_slots) continue;
-      p.slots[i] = page[u] >= 0 && page[u] < p.n_pages
-                       ? static_cast<long long>(page[u]) * p.P + row[u]
-                       : -1;
-      p.positions[i] = pos[u];
+      const long long j = j0 + static_cast<long long>(u) * step;
+      if (j < R) p.ring[at(tail0, static_cast<int>(j))] = entry[u];
     }
-  }
-  for (int j = start; j < N; j += step) {
-    const int b = last_at_most(cu_need, p.B, j);
-    p.table[b * p.table_sb + pages_of(len_s[b], p.P) + (j - cu_need[b])] = p.ring[at(head0, j)];
-  }
-  for (int j = start; j < R; j += step) {
-    const int b = last_at_most(cu_back, p.B, j);
-    p.ring[at(tail0, j)] = p.table[b * p.table_sb + (j - cu_back[b])];
   }
   for (int b = start; b <= p.B; b += step) {
     p.cu[b] = cu_tok[b];
@@ -226,6 +266,48 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     p.state_out[0] = head + N;
     p.state_out[1] = tail + R;
     p.status[0] = status;
+  }
+}
+
+// Slots and positions of a planned step's tokens, from what the plan wrote:
+// offsets, new lengths and tables.  A warp takes 32 V neighbours, a lane every
+// 32nd of them (so that stores coalesce): a search where a lane enters another
+// request.  Grid: ceil(n_slots / (V kSlotsThreads)).
+constexpr int kSlotsThreads = 256;
+constexpr int kSlotsV = 4;
+__global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PlanParams p) {
+  dec_grid_dep_wait();
+  dec_grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long i0 =
+      32LL * kSlotsV * (static_cast<long long>(blockIdx.x) * (kSlotsThreads / 32) + warp);
+  const int T = p.cu[p.B];
+  int page[kSlotsV], pos[kSlotsV], row[kSlotsV];
+  int b = 0, end = 0, shift = 0;
+#pragma unroll
+  for (int u = 0; u < kSlotsV; ++u) {
+    page[u] = pos[u] = -1;
+    row[u] = 0;
+    const long long i = i0 + 32 * u + lane;
+    if (i >= T) continue;
+    if (u == 0 || i >= end) {
+      b = last_at_most(p.cu, b, p.B, static_cast<int>(i));
+      end = p.cu[b + 1];
+      shift = p.lengths_out[b] - end;  // length before the step - cu[b]
+    }
+    pos[u] = static_cast<int>(i) + shift;
+    const int lp = p.by_P(pos[u]);
+    row[u] = pos[u] - lp * p.P;
+    page[u] = p.table[b * p.table_sb + lp];
+  }
+#pragma unroll
+  for (int u = 0; u < kSlotsV; ++u) {
+    const long long i = i0 + 32 * u + lane;
+    if (i >= p.n_slots) continue;
+    p.slots[i] = page[u] >= 0 && page[u] < p.n_pages
+                     ? static_cast<long long>(page[u]) * p.P + row[u]
+                     : -1;
+    p.positions[i] = pos[u];
   }
 }
 

@@ -373,7 +373,7 @@ CATTN_API cattn_status attn_decode(const void* q, cattn_layout lq, const void* k
  *               ring_state, cu_new = 0, slots = positions = -1
  *
  * Pages belong to one request.  Apart from the pairs named above no two
- * arrays may overlap.  One launch.  Errors: CATTN_ERR_INVALID_ARG,
+ * arrays may overlap.  One launch, two above 16,384 slots.  Errors: CATTN_ERR_INVALID_ARG,
  * CATTN_ERR_UNSUPPORTED (B above 8192, device), CATTN_ERR_CUDA. */
 CATTN_API cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
                                        int32_t* block_table, long long table_stride,
@@ -589,9 +589,9 @@ CATTN_API cattn_status cattn_selftest_wait_timeout_ws(uint32_t timeout_us, void*
  * launching stream.  cattn_timing_read() waits for the recorded events and
  * returns, per kernel, the summed device time in ms and the launch count,
  * then forgets them.  Kernel index: 0 forward, 1 backward preprocess,
- * 2 backward main, 3 dQ convert, 4 decode (attn_decode, or the two kernels
- * of attn_decode_paged and _sparse together), 5 attn_paged_plan and
- * attn_cache_append, 6 attn_page_select (its two kernels together).
+ * 2 backward main, 3 dQ convert, 4 decode (attn_decode, attn_decode_paged or
+ * _sparse), 5 attn_paged_plan or attn_cache_append, 6 attn_page_select (the
+ * launches of a call together).
  * n = length of both output arrays (indices >= n are dropped).  Not
  * for use while a stream is being captured into a CUDA graph. */
 CATTN_API void cattn_timing_enable(int enable);

@@ -108,7 +108,7 @@ static void decode() {
   put(p.lse, rows * 4);
 }
 
-// params: B width n_pages P n_slots ctas in_place threads
+// params: B width n_pages P n_slots ctas in_place threads prompts
 // arrays: asked, lengths, table, ring, state
 static void plan() {
   const int64_t* a = in<int64_t>(0);
@@ -128,8 +128,14 @@ static void plan() {
   p.slots = out<long long>(p.n_slots);
   p.positions = out<int>(p.n_slots);
   p.status = out<int>(1);
-  emu::launch_ex(ctas, a[7], plan_smem_bytes(p.B), ctas, paged_plan_kernel, p,
+  plan_divider(p);
+  emu::launch_ex(ctas, a[7], plan_smem_bytes(p.B), ctas,
+                 a[8] ? paged_plan_kernel<false> : paged_plan_kernel<true>, p,
                  static_cast<int>(ctas));
+  const int64_t per = kSlotsV * kSlotsThreads;
+  if (a[8])
+    emu::launch_ex(static_cast<unsigned>((p.n_slots + per - 1) / per), kSlotsThreads, 0, 1,
+                   paged_slots_kernel, p);
   put(p.lengths_out, 4ull * p.B);
   put(p.state_out, 16);
   put(p.cu, 4ull * (p.B + 1));

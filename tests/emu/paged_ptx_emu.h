@@ -10,8 +10,11 @@
 
 #include "decode_ptx_emu.h"
 
-struct alignas(8) int2 {
-  int x, y;
+struct alignas(16) int4 {
+  int x, y, z, w;
+};
+struct alignas(16) longlong2 {
+  long long x, y;
 };
 
 namespace cattn {

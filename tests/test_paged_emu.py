@@ -187,9 +187,9 @@ def test_sparse(emu, Tq, G):
 # ------------------------------------------------------------------- plan
 
 def run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas=1, in_place=False,
-             threads=256):
+             threads=256, prompts=False):
     B, width = table.shape
-    raw = emu("plan", [B, width, len(ring), P, n_slots, ctas, int(in_place), threads],
+    raw = emu("plan", [B, width, len(ring), P, n_slots, ctas, int(in_place), threads, int(prompts)],
               np.array(asked, np.int32), np.array(lengths, np.int32), table.astype(np.int32),
               np.array(ring, np.int32), np.array(state, np.int64))
     got = take(raw, (np.int32, B), (np.int64, 2), (np.int32, B + 1), (np.int64, n_slots),
@@ -227,6 +227,7 @@ def test_plan(emu, B, P, longest, most, ctas, threads, in_place):
     asked, lengths, table, ring, state = plan_inputs(B + P, B, P, longest, most)
     n_slots = int(np.maximum(asked, 0).sum()) + 3
     want = run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas, in_place, threads)
+    run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas, in_place, threads, True)
     assert want["status"] == opaged.OK
 
 
