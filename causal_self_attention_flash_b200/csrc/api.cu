@@ -761,7 +761,21 @@ cattn_status check_paged(int B, int H, int Hkv, int D, int n_pages, int P, int w
 }
 
 template <int D, bool UP>
-cattn_status paged_impl(const PagedParams& p, int grid, int dev, cudaStream_t s) {
+cattn_status paged_item_impl(const PagedParams& p, int ctas, int dev, cudaStream_t s) {
+  cattn_status st = ensure_smem(dev, 87 + 2 * d_index(D) + UP, paged_item_kernel<D, UP>,
+                                paged_smem_bytes(D));
+  if (st != CATTN_OK) return st;
+  clear_stale_error();
+  LaunchTimer t(K_DECODE, s);
+  const long long items = static_cast<long long>(p.B) * p.Hkv * p.n_tiles;
+  const cudaError_t e = launch_cluster(paged_item_kernel<D, UP>, items * ctas, kPagedThreads, ctas,
+                                       paged_smem_bytes(D), s, p, ctas);
+  return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
+}
+
+template <int D, bool UP>
+cattn_status paged_impl(const PagedParams& p, int ctas, int grid, int dev, cudaStream_t s) {
+  if (ctas > 0) return paged_item_impl<D, UP>(p, ctas, dev, s);
   cattn_status st = ensure_smem(dev, 68 + 2 * d_index(D) + UP, paged_decode_kernel<D, UP>,
                                 paged_smem_bytes(D));
   if (st != CATTN_OK) return st;
@@ -840,13 +854,14 @@ cattn_status paged_decode(const void* q, cattn_layout lq, const void* k, cattn_l
   if (grid > slots) grid = slots;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int gr = static_cast<int>(grid);
+  const int ctas = paged_item_ctas(static_cast<long long>(B) * Hkv * p.n_tiles, chunks);
   const bool up = p.rows > 8;
   switch (D) {
-    case 16: return up ? paged_impl<16, true>(p, gr, dev, s) : paged_impl<16, false>(p, gr, dev, s);
-    case 32: return up ? paged_impl<32, true>(p, gr, dev, s) : paged_impl<32, false>(p, gr, dev, s);
-    case 64: return up ? paged_impl<64, true>(p, gr, dev, s) : paged_impl<64, false>(p, gr, dev, s);
+    case 16: return up ? paged_impl<16, true>(p, ctas, gr, dev, s) : paged_impl<16, false>(p, ctas, gr, dev, s);
+    case 32: return up ? paged_impl<32, true>(p, ctas, gr, dev, s) : paged_impl<32, false>(p, ctas, gr, dev, s);
+    case 64: return up ? paged_impl<64, true>(p, ctas, gr, dev, s) : paged_impl<64, false>(p, ctas, gr, dev, s);
     case 128:
-      return up ? paged_impl<128, true>(p, gr, dev, s) : paged_impl<128, false>(p, gr, dev, s);
+      return up ? paged_impl<128, true>(p, ctas, gr, dev, s) : paged_impl<128, false>(p, ctas, gr, dev, s);
   }
   return CATTN_ERR_UNSUPPORTED;
 }

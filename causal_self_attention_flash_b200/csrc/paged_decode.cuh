@@ -126,6 +126,11 @@ struct PagedPlace {
   int b, ht, c, n, len;
 };
 
+// A key: its page (-1: none is held), its row there, its position.
+struct PagedKey {
+  int page, row, pos;
+};
+
 template <int D>
 __device__ __forceinline__ void paged_next(const PagedParams& p, int HT, PagedPlace& x) {
   if (++x.c < x.n) return;
@@ -211,7 +216,6 @@ struct PagedWarp {
   float o[NO][4];              // running state of rows g (and g + 8)
   float m_run[NR], l_run[NR];  // (l is the lane's part)
   int row_pos[NR];             // the rows' positions
-  int key_page, key_row, key_pos;  // looked up: the lane's key of the next chunk
 
   __device__ __forceinline__ PagedWarp(const PagedParams& params, uint8_t* smem, int warp,
                                        int lane_)
@@ -232,10 +236,8 @@ struct PagedWarp {
   }
 
   // The page, the row in it and the position of the lane's key of chunk x.
-  __device__ __forceinline__ void look_up(const PagedPlace& x) {
-    key_page = -1;
-    key_pos = kPagedNone;
-    key_row = 0;
+  __device__ __forceinline__ PagedKey look_up(const PagedPlace& x) const {
+    PagedKey key{-1, 0, kPagedNone};
     const int vk = x.c * CK + lane;
     const int li = vk / p.P;
     const int row = vk - li * p.P;
@@ -251,27 +253,24 @@ struct PagedWarp {
     }
     if (lp >= 0 && lp < p.width && lp * p.P + row < x.len) {
       const int page = p.table[x.b * p.table_sb + lp];
-      if (page >= 0 && page < p.n_pages) {
-        key_page = page;
-        key_row = row;
-        key_pos = lp * p.P + row;
-      }
+      if (page >= 0 && page < p.n_pages) key = PagedKey{page, row, lp * p.P + row};
     }
+    return key;
   }
 
-  // Chunk x (looked up) into ring slot `slot`; rows of keys that are not
+  // A chunk of item (b, ht) into ring slot `slot`; rows of keys that are not
   // held are zero-filled (and masked in chunk()).
-  __device__ __forceinline__ void issue(const PagedPlace& x, int slot) {
+  __device__ __forceinline__ void issue(int ht, const PagedKey& key, int slot) {
     uint8_t* sk = ring + slot * CB;
     uint8_t* sv = sk + TILE;
-    const int h = x.ht / p.n_tiles;
+    const int h = ht / p.n_tiles;
     const __nv_bfloat16* kb = p.k + h * p.k_sh;
     const __nv_bfloat16* vb = p.v + h * p.v_sh;
-    slot_pos[slot * 32 + lane] = key_pos;
+    slot_pos[slot * 32 + lane] = key.pos;
 #pragma unroll
     for (int u = 0; u < TILE / 16 / 32; ++u) {
       const int piece = lane + 32 * u, row = piece / PC, pc = piece - (piece / PC) * PC;
-      const int page = dec_shfl(key_page, row), in = dec_shfl(key_row, row);
+      const int page = dec_shfl(key.page, row), in = dec_shfl(key.row, row);
       const bool ok = page >= 0;
       const long long pg = ok ? page : 0;
       dec_cp_async16(sk + dec_swz<D>(row, pc), kb + pg * p.k_sp + in * p.k_st + pc * 8, ok);
@@ -510,6 +509,118 @@ __device__ __forceinline__ void paged_join(float m, float l, float& M, float& L,
   L = fmaf(L, fa, fb * l);
 }
 
+// Row r's column d over the CTA's warps, from the merge area: M, L and the sum.
+template <int D>
+__device__ __forceinline__ float paged_cta_sum(const PagedMerge& a, int r, int d, float& M,
+                                               float& L) {
+  float acc = 0.f, fa, fb;
+  M = -INFINITY;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kPagedWarps; ++w) {
+    const float2 ml = a.ml[w * kPagedRows + r];
+    paged_join(ml.x, ml.y, M, L, fa, fb);
+    acc = fmaf(acc, fa, fb * a.ov[(w * kPagedRows + r) * D + d]);
+  }
+  return acc;
+}
+
+// o and lse of row r (of tile r0), column d of item x.
+__device__ __forceinline__ void paged_write(const PagedParams& p, const PagedPlace& x, int h,
+                                            int gr, int d, float M, float L, float acc) {
+  const int gh = gr / p.Tq, t = gr - gh * p.Tq;
+  const long long hq = static_cast<long long>(h) * (p.rows / p.Tq) + gh;
+  p.o[x.b * p.o_sb + hq * p.o_sh + t * p.o_st + d] =
+      __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+  if (d == 0) p.lse[(x.b * static_cast<long long>(p.H) + hq) * p.Tq + t] = paged_lse(M, L);
+}
+
+// One item per thread-block cluster: for calls whose longest item is short, or
+// whose items are few.  The warps of its CTAs take turns at its chunks; their
+// results are joined in shared memory, the CTAs' in distributed shared memory.
+// Nothing to scan, no workspace, one launch.  Grid: items * ctas in clusters of
+// ctas.
+template <int D, bool UP>
+__global__ void __launch_bounds__(kPagedThreads, 2)
+    paged_item_kernel(const PagedParams p, int ctas) {
+  dec_grid_dep_wait();
+  dec_grid_dep_launch();
+  uint8_t* smem = dec_dynamic_smem();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int HT = p.Hkv * p.n_tiles, item = static_cast<int>(blockIdx.x) / ctas;
+  const int rank = static_cast<int>(blockIdx.x) - item * ctas;
+  PagedPlace x;
+  x.b = item / HT;
+  x.ht = item - x.b * HT;
+  x.len = p.lengths[x.b];
+  x.n = paged_chunks<D>(p, x.len);
+  x.c = rank * kPagedWarps + warp;
+  const int step = ctas * kPagedWarps, h = x.ht / p.n_tiles;
+  const int left = x.n > x.c ? (x.n - x.c + step - 1) / step : 0;
+  PagedWarp<D, UP> k(p, smem, warp, lane);
+  // the first chunks' keys are looked up together, then one ahead
+  PagedKey key[kPagedStages], next{-1, 0, kPagedNone};
+  auto look_up = [&](int i) {
+    PagedPlace y = x;
+    y.c = x.c + i * step;
+    return k.look_up(y);
+  };
+#pragma unroll
+  for (int i = 0; i < kPagedStages; ++i)
+    if (i < left) key[i] = look_up(i);
+#pragma unroll
+  for (int i = 0; i < kPagedStages; ++i) {
+    if (i < left) k.issue(x.ht, key[i], i);
+    dec_cp_async_commit();
+  }
+  if (kPagedStages < left) next = look_up(kPagedStages);
+  k.begin(x);
+  int slot = 0;
+  for (int i = 0; i < left; ++i) {
+    dec_cp_async_wait<kPagedStages - 1>();
+    __syncwarp();  // every lane's pieces of the chunk are in shared memory
+    k.chunk(slot, x.len);
+    __syncwarp();  // every lane has read the slot: refill it
+    if (i + kPagedStages < left) {
+      k.issue(x.ht, next, slot);
+      if (i + kPagedStages + 1 < left) next = look_up(i + kPagedStages + 1);
+    }
+    dec_cp_async_commit();
+    slot = slot + 1 == kPagedStages ? 0 : slot + 1;
+  }
+  dec_cp_async_wait<0>();
+  const PagedMerge a = paged_merge_area<D>(smem);
+  __syncthreads();  // every warp is done with its ring
+  k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, kPagedRows);
+  __syncthreads();
+  const int r0 = (x.ht - h * p.n_tiles) * kPagedRows;
+  const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;
+  for (int i = tid; i < rows * D; i += kPagedThreads) {
+    const int r = i / D, d = i - r * D;
+    float M, L;
+    const float acc = paged_cta_sum<D>(a, r, d, M, L);
+    if (ctas == 1) {
+      paged_write(p, x, h, r0 + r, d, M, L, acc);
+    } else {
+      a.cta_ov[i] = acc;
+      if (d == 0) a.cta_ml[r] = float2{M, L};
+    }
+  }
+  if (ctas == 1) return;
+  dec_cluster_sync();  // every CTA's part is in its shared memory
+  for (int i = rank * kPagedThreads + tid; i < rows * D; i += ctas * kPagedThreads) {
+    const int r = i / D, d = i - r * D;
+    float M = -INFINITY, L = 0.f, acc = 0.f, fa, fb;
+    for (int c = 0; c < ctas; ++c) {
+      const float m = dec_cluster_ld(&a.cta_ml[r].x, c), l = dec_cluster_ld(&a.cta_ml[r].y, c);
+      paged_join(m, l, M, L, fa, fb);
+      acc = fmaf(acc, fa, fb * dec_cluster_ld(a.cta_ov + i, c));
+    }
+    paged_write(p, x, h, r0 + r, d, M, L, acc);
+  }
+  dec_cluster_sync();  // no CTA leaves while its shared memory is read
+}
+
 // Grid: up to kPagedMaxCtas CTAs of kPagedThreads, paged_smem_bytes(D) of
 // dynamic shared memory.
 //
@@ -580,21 +691,29 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
 
   PagedWarp<D, UP> k(p, smem, warp, lane);
   PagedPlace get = use;
-  int to_issue = left;
-  auto issue = [&](int slot) {  // the next chunk, and the look-up of the one behind it
-    k.issue(get, slot);
-    if (--to_issue > 0) {
+  int to_look = left;
+  PagedKey key[kPagedStages], next{-1, 0, kPagedNone};
+  int hts[kPagedStages];
+  auto look_up = [&](PagedKey& to) {  // the next chunk's keys, and on to the one behind it
+    to = k.look_up(get);
+    const int ht = get.ht;
+    if (--to_look > 0) {
       if (together) get.c += step; else paged_next<D>(p, HT, get);
-      k.look_up(get);
     }
+    return ht;
   };
-  if (to_issue > 0) k.look_up(get);
-  // one commit group per ring slot, empty when the run is shorter
+  // the first chunks' keys are looked up together, then one ahead; one commit
+  // group per ring slot, empty when the run is shorter
+#pragma unroll
+  for (int i = 0; i < kPagedStages; ++i)
+    if (i < left) hts[i] = look_up(key[i]);
 #pragma unroll
   for (int i = 0; i < kPagedStages; ++i) {
-    if (to_issue > 0) issue(i);
+    if (i < left) k.issue(hts[i], key[i], i);
     dec_cp_async_commit();
   }
+  int next_ht = 0, to_issue = left - kPagedStages;
+  if (to_issue > 0) next_ht = look_up(next);
 
   bool begins = use.c == 0;  // the current item's first chunk is this warp's
   bool fresh = true;
@@ -609,7 +728,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     __syncwarp();  // every lane's pieces of the chunk are in shared memory
     k.chunk(slot, use.len);
     __syncwarp();  // every lane has read the slot: refill it
-    if (to_issue > 0) issue(slot);
+    if (to_issue > 0) {
+      k.issue(next_ht, next, slot);
+      if (--to_issue > 0) next_ht = look_up(next);
+    }
     dec_cp_async_commit();
     slot = slot + 1 == kPagedStages ? 0 : slot + 1;
     --left;
@@ -648,20 +770,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     const long long part = (2LL * cta * kPagedWarps + (first.c == 0)) * p.R;
     for (int i = tid; i < rows * D && first.b < p.B; i += kPagedThreads) {
       const int r = i / D, d = i - r * D;
-      float M = -INFINITY, L = 0.f, acc = 0.f, fa, fb;
-#pragma unroll
-      for (int w = 0; w < kPagedWarps; ++w) {
-        const float2 ml = a.ml[w * kPagedRows + r];
-        paged_join(ml.x, ml.y, M, L, fa, fb);
-        acc = fmaf(acc, fa, fb * a.ov[(w * kPagedRows + r) * D + d]);
-      }
+      float M, L;
+      const float acc = paged_cta_sum<D>(a, r, d, M, L);
       if (whole) {
-        int t;
-        const long long hq = k.row_head(h, r0 + r, &t);
-        p.o[first.b * p.o_sb + hq * p.o_sh + t * p.o_st + d] =
-            __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
-        if (d == 0)
-          p.lse[(first.b * static_cast<long long>(p.H) + hq) * p.Tq + t] = paged_lse(M, L);
+        paged_write(p, first, h, r0 + r, d, M, L, acc);
       } else {
         p.part_o[(part + r) * D + d] = acc;
         if (d == 0) p.part_ml[part + r] = float2{M, L};
@@ -674,6 +786,16 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
   if (together ? warp > 0 : E == S || s == S + static_cast<long long>(warp + 1) * share / kPagedWarps)
     if (lane < p.R) p.part_ml[2LL * gw * p.R + lane] = float2{-INFINITY, 0.f};
   if (lane == 0) p.cuts[gw] = cut;
+}
+
+// CTAs per item of paged_item_kernel, or 0 for paged_decode_kernel, from the
+// items and the chunks that the table (the list) has room for; the lengths are
+// not known here.
+__host__ __device__ constexpr int paged_item_ctas(long long items, long long chunks) {
+  int ctas = 1;
+  while (ctas < 8 && 2 * ctas * items <= kPagedMaxCtas && chunks > 2 * kPagedWarps * ctas)
+    ctas *= 2;
+  return items * ctas <= 2 * kPagedMaxCtas && chunks <= 16LL * kPagedWarps * ctas ? ctas : 0;
 }
 
 // Joins the parts of the cut items:  M = max m_i,

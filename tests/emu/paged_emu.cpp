@@ -55,13 +55,20 @@ static void put(const void* p, size_t bytes) {
 
 template <int D, bool UP>
 static void run_decode(const PagedParams& p, int grid) {
+  if (grid < 0) {
+    emu::launch_ex(static_cast<unsigned>(p.B * p.Hkv * p.n_tiles * -grid), kPagedThreads,
+                   paged_smem_bytes(D), static_cast<unsigned>(-grid), paged_item_kernel<D, UP>, p,
+                   -grid);
+    return;
+  }
   emu::launch_ex(grid, kPagedThreads, paged_smem_bytes(D), 1, paged_decode_kernel<D, UP>, p);
   const int n_y = paged_merge_y(p.R);
   emu::launch_ex(grid * n_y, kMergeThreads, paged_merge_smem_bytes(D), 1, paged_merge_kernel<D>,
                  p, n_y);
 }
 
-// params: B H Hkv Tq D n_pages P width n_sel grid layout; scale as float
+// params: B H Hkv Tq D n_pages P width n_sel grid layout (grid < 0: -grid CTAs
+//         per item); scale as float
 // arrays: q, k, v (layout 0: (n_pages, Hkv, P, D), 1: (n_pages, P, Hkv, D)),
 //         table, lengths, pages, scale
 static void decode() {
@@ -93,9 +100,10 @@ static void decode() {
   const size_t rows = static_cast<size_t>(p.B) * p.H * p.Tq;
   p.o = out<__nv_bfloat16>(rows * D);
   p.lse = out<float>(rows);
-  p.cuts = out<PagedCut>(static_cast<size_t>(grid) * kPagedWarps);
-  p.part_ml = out<float2>(2ull * grid * kPagedWarps * p.R);
-  p.part_o = out<float>(2ull * grid * kPagedWarps * p.R * D);
+  const size_t warps = grid > 0 ? static_cast<size_t>(grid) * kPagedWarps : 0;
+  p.cuts = out<PagedCut>(warps);
+  p.part_ml = out<float2>(2 * warps * p.R);
+  p.part_o = out<float>(2 * warps * p.R * D);
   const bool up = p.rows > 8;
   switch (D) {
     case 16: up ? run_decode<16, true>(p, grid) : run_decode<16, false>(p, grid); break;

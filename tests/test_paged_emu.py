@@ -113,6 +113,7 @@ def run_decode(emu, lengths, Hkv, G, Tq, D, P, grid, *, layout=1, spare=0, holes
 ])
 def test_decode(emu, lengths, Hkv, G, Tq, D, P, grid):
     run_decode(emu, lengths, Hkv, G, Tq, D, P, grid, spare=2)
+    run_decode(emu, lengths, Hkv, G, Tq, D, P, -(1 + len(lengths) % 3), spare=2, seed=9)
 
 
 @pytest.mark.parametrize("layout", [0, 1])
@@ -129,9 +130,10 @@ def test_decode_many_requests(emu):
 @pytest.mark.parametrize("Tq", [1, 3])
 def test_decode_pages_that_are_not_held(emu, Tq):
     """-1 and page numbers outside the pool: nothing is read there"""
-    run_decode(emu, [100, 40, 20], 1, 2, Tq, 64, 16, 2,
-               holes=[((0, 0), -1), ((0, 3), 10 ** 6), ((1, 2), -7), ((2, 0), 1 << 30),
-                      ((2, 1), -1)])
+    for grid in (2, -1, -2):
+        run_decode(emu, [100, 40, 20], 1, 2, Tq, 64, 16, grid,
+                   holes=[((0, 0), -1), ((0, 3), 10 ** 6), ((1, 2), -7), ((2, 0), 1 << 30),
+                          ((2, 1), -1)])
 
 
 def test_decode_longer_than_the_table(emu):
@@ -180,8 +182,9 @@ def test_sparse(emu, Tq, G):
     pages[1, :, :2] = [0, 1]
     pages[2, 0] = [0, 99, -4, 2]        # entries that list nothing
     pages[2, 1] = [2, 1, 0, 7]          # any order; the fourth is behind the last page
-    run_decode(emu, [100, 20, 45], 2, G, Tq, 64, 16, 2, spare=1, pages=pages,
-               holes=[((0, 5), -1)])
+    for grid in (2, -2):
+        run_decode(emu, [100, 20, 45], 2, G, Tq, 64, 16, grid, spare=1, pages=pages,
+                   holes=[((0, 5), -1)])
 
 
 # ------------------------------------------------------------------- plan
