@@ -760,34 +760,40 @@ cattn_status check_paged(int B, int H, int Hkv, int D, int n_pages, int P, int w
   return CATTN_OK;
 }
 
-template <int D, bool UP>
-cattn_status paged_item_impl(const PagedParams& p, int ctas, int dev, cudaStream_t s) {
-  cattn_status st = ensure_smem(dev, 87 + 2 * d_index(D) + UP, paged_item_kernel<D, UP>,
-                                paged_smem_bytes(D));
+template <int D, bool UP, bool MULTI>
+cattn_status paged_impl(const PagedParams& p, int ctas, int grid, int dev, cudaStream_t s) {
+  const bool item = ctas > 0;
+  const auto flat_kernel = paged_decode_kernel<D, UP, MULTI>;
+  const auto item_kernel = paged_item_kernel<D, UP, MULTI>;
+  const unsigned bit = 87 + 4 * d_index(D) + 2 * UP + MULTI;
+  cattn_status st = item ? ensure_smem(dev, bit, item_kernel, paged_smem_bytes(D))
+                         : ensure_smem(dev, bit + 16, flat_kernel, paged_smem_bytes(D));
   if (st != CATTN_OK) return st;
   clear_stale_error();
   LaunchTimer t(K_DECODE, s);
   const long long items = static_cast<long long>(p.B) * p.Hkv * p.n_tiles;
-  const cudaError_t e = launch_cluster(paged_item_kernel<D, UP>, items * ctas, kPagedThreads, ctas,
-                                       paged_smem_bytes(D), s, p, ctas);
+  cudaError_t e = cudaSuccess;
+  if (item) {
+    e = launch_cluster(item_kernel, items * ctas, kPagedThreads, ctas, paged_smem_bytes(D), s, p,
+                       ctas);
+  } else {
+    e = launch_dependent(true, flat_kernel, dim3(grid), dim3(kPagedThreads), paged_smem_bytes(D),
+                         s, p);
+    if (e == cudaSuccess)
+      e = launch_dependent(true, paged_merge_kernel<D>, dim3(grid * paged_merge_y(p.R)),
+                           dim3(kMergeThreads), paged_merge_smem_bytes(D), s, p,
+                           paged_merge_y(p.R));
+  }
   return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
 }
 
-template <int D, bool UP>
-cattn_status paged_impl(const PagedParams& p, int ctas, int grid, int dev, cudaStream_t s) {
-  if (ctas > 0) return paged_item_impl<D, UP>(p, ctas, dev, s);
-  cattn_status st = ensure_smem(dev, 68 + 2 * d_index(D) + UP, paged_decode_kernel<D, UP>,
-                                paged_smem_bytes(D));
-  if (st != CATTN_OK) return st;
-  clear_stale_error();
-  LaunchTimer t(K_DECODE, s);
-  cudaError_t e = launch_dependent(true, paged_decode_kernel<D, UP>, dim3(grid),
-                                   dim3(kPagedThreads), paged_smem_bytes(D), s, p);
-  if (e == cudaSuccess)
-    e = launch_dependent(true, paged_merge_kernel<D>, dim3(grid * paged_merge_y(p.R)),
-                         dim3(kMergeThreads), paged_merge_smem_bytes(D), s, p,
-                         paged_merge_y(p.R));
-  return e == cudaSuccess ? CATTN_OK : cuda_fail(e);
+template <int D>
+cattn_status paged_dispatch(const PagedParams& p, int ctas, int grid, int dev, cudaStream_t s) {
+  const bool up = p.rows > 8, multi = p.Tq > 1;
+  if (up) return multi ? paged_impl<D, true, true>(p, ctas, grid, dev, s)
+                       : paged_impl<D, true, false>(p, ctas, grid, dev, s);
+  return multi ? paged_impl<D, false, true>(p, ctas, grid, dev, s)
+               : paged_impl<D, false, false>(p, ctas, grid, dev, s);
 }
 
 // attn_decode_paged (pages == nullptr) and attn_decode_sparse.
@@ -855,13 +861,11 @@ cattn_status paged_decode(const void* q, cattn_layout lq, const void* k, cattn_l
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int gr = static_cast<int>(grid);
   const int ctas = paged_item_ctas(static_cast<long long>(B) * Hkv * p.n_tiles, chunks);
-  const bool up = p.rows > 8;
   switch (D) {
-    case 16: return up ? paged_impl<16, true>(p, ctas, gr, dev, s) : paged_impl<16, false>(p, ctas, gr, dev, s);
-    case 32: return up ? paged_impl<32, true>(p, ctas, gr, dev, s) : paged_impl<32, false>(p, ctas, gr, dev, s);
-    case 64: return up ? paged_impl<64, true>(p, ctas, gr, dev, s) : paged_impl<64, false>(p, ctas, gr, dev, s);
-    case 128:
-      return up ? paged_impl<128, true>(p, ctas, gr, dev, s) : paged_impl<128, false>(p, ctas, gr, dev, s);
+    case 16: return paged_dispatch<16>(p, ctas, gr, dev, s);
+    case 32: return paged_dispatch<32>(p, ctas, gr, dev, s);
+    case 64: return paged_dispatch<64>(p, ctas, gr, dev, s);
+    case 128: return paged_dispatch<128>(p, ctas, gr, dev, s);
   }
   return CATTN_ERR_UNSUPPORTED;
 }

@@ -27,9 +27,10 @@
 //   - an item that ends inside its warp's run is written out directly; a cut
 //     item leaves (m, l, o) per warp in the workspace and merge_kernel joins
 //     them, in the order of the keys, so results repeat bit for bit.
-// p enters the second product as a bf16 pair (hi + lo, about 16 bits): the
-// tensor pipe has room (the kernel waits for memory), and o then carries no
-// rounding but its own to bf16.
+// p enters the second product as a bf16 pair (hi + lo, about 16 bits), so that
+// o carries no rounding but its own to bf16.  With at most 8 rows that costs no
+// instruction: hi takes the fragment's rows 0 .. 7, lo its rows 8 .. 15, and
+// the two halves of the accumulator are added at the end.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -126,9 +127,11 @@ struct PagedPlace {
   int b, ht, c, n, len;
 };
 
-// A key: its page (-1: none is held), its row there, its position.
+// A key: where its rows of K and V begin (elements from head 0 of the pool; -1:
+// it is not held), and its position.
 struct PagedKey {
-  int page, row, pos;
+  long long k, v;
+  int pos;
 };
 
 template <int D>
@@ -195,8 +198,9 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
 }
 
 // One warp's work on chunks: its ring of shared memory slots and the running
-// state of the item it is in.  UP: rows 8 .. 15 of the tile are used.
-template <int D, bool UP>
+// state of the item it is in.  UP: rows 8 .. 15 of the tile are used.  MULTI:
+// several new positions (Tq > 1), so that rows may see different keys.
+template <int D, bool UP, bool MULTI>
 struct PagedWarp {
   static constexpr int CK = paged_chunk(D);  // keys per chunk
   static constexpr int PC = D / 8;           // 16-byte pieces per row
@@ -206,10 +210,11 @@ struct PagedWarp {
   static constexpr int TILE = CK * D * 2;    // bytes of K (of V) per chunk
   static constexpr int CB = 2 * TILE;
   static constexpr int NR = UP ? 2 : 1;      // fragment rows of a lane: g, g + 8
-  static_assert(TILE / 16 % 32 == 0 && CK % 16 == 0 && CK <= 32, "chunk");
+  static_assert(TILE / 16 % 32 == 0 && CK % 16 == 0 && CK <= 32 && 32 % PC == 0, "chunk");
 
   const PagedParams& p;
   int lane, g, t4;             // lane, fragment row, column pair
+  bool same;                   // K and V have one layout
   uint8_t* ring;
   int* slot_pos;               // positions of the slots' keys
   uint32_t qa[KS][4];          // query rows as mma A fragments
@@ -219,7 +224,8 @@ struct PagedWarp {
 
   __device__ __forceinline__ PagedWarp(const PagedParams& params, uint8_t* smem, int warp,
                                        int lane_)
-      : p(params), lane(lane_), g(lane_ >> 2), t4(lane_ & 3) {
+      : p(params), lane(lane_), g(lane_ >> 2), t4(lane_ & 3),
+        same(params.k_sp == params.v_sp && params.k_st == params.v_st) {
     ring = smem + warp * (kPagedStages * CB);
     slot_pos = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + warp * kPagedStages * 32;
     clear();
@@ -237,7 +243,7 @@ struct PagedWarp {
 
   // The page, the row in it and the position of the lane's key of chunk x.
   __device__ __forceinline__ PagedKey look_up(const PagedPlace& x) const {
-    PagedKey key{-1, 0, kPagedNone};
+    PagedKey key{-1, -1, kPagedNone};
     const int vk = x.c * CK + lane;
     const int li = vk / p.P;
     const int row = vk - li * p.P;
@@ -253,28 +259,29 @@ struct PagedWarp {
     }
     if (lp >= 0 && lp < p.width && lp * p.P + row < x.len) {
       const int page = p.table[x.b * p.table_sb + lp];
-      if (page >= 0 && page < p.n_pages) key = PagedKey{page, row, lp * p.P + row};
+      if (page >= 0 && page < p.n_pages)
+        key = PagedKey{page * p.k_sp + row * p.k_st, page * p.v_sp + row * p.v_st, lp * p.P + row};
     }
     return key;
   }
 
   // A chunk of item (b, ht) into ring slot `slot`; rows of keys that are not
-  // held are zero-filled (and masked in chunk()).
+  // held are zero-filled (and masked in chunk()).  A lane copies the same
+  // 16 bytes of every (32 / PC)-th row.
   __device__ __forceinline__ void issue(int ht, const PagedKey& key, int slot) {
     uint8_t* sk = ring + slot * CB;
     uint8_t* sv = sk + TILE;
     const int h = ht / p.n_tiles;
-    const __nv_bfloat16* kb = p.k + h * p.k_sh;
-    const __nv_bfloat16* vb = p.v + h * p.v_sh;
+    const __nv_bfloat16* kb = p.k + h * p.k_sh + (lane % PC) * 8;
+    const __nv_bfloat16* vb = p.v + h * p.v_sh + (lane % PC) * 8;
     slot_pos[slot * 32 + lane] = key.pos;
 #pragma unroll
     for (int u = 0; u < TILE / 16 / 32; ++u) {
-      const int piece = lane + 32 * u, row = piece / PC, pc = piece - (piece / PC) * PC;
-      const int page = dec_shfl(key.page, row), in = dec_shfl(key.row, row);
-      const bool ok = page >= 0;
-      const long long pg = ok ? page : 0;
-      dec_cp_async16(sk + dec_swz<D>(row, pc), kb + pg * p.k_sp + in * p.k_st + pc * 8, ok);
-      dec_cp_async16(sv + dec_swz<D>(row, pc), vb + pg * p.v_sp + in * p.v_st + pc * 8, ok);
+      const int row = lane / PC + 32 / PC * u, at = dec_swz<D>(row, lane % PC);
+      const long long ko = dec_shfl(key.k, row), vo = same ? ko : dec_shfl(key.v, row);
+      const bool ok = ko >= 0;
+      dec_cp_async16(sk + at, kb + (ok ? ko : 0), ok);
+      dec_cp_async16(sv + at, vb + (ok ? vo : 0), ok);
     }
   }
 
@@ -335,7 +342,7 @@ struct PagedWarp {
     }
     // keys that are not held, and keys behind a row's position
     const int my_pos = lane < CK ? pos[lane] : -1;
-    const bool masked = dec_ballot(my_pos > pos0) != 0u;
+    const bool masked = dec_ballot(MULTI ? my_pos > pos0 : my_pos == kPagedNone) != 0u;
     if (masked) {
 #pragma unroll
       for (int nt = 0; nt < NS; ++nt)
@@ -344,7 +351,7 @@ struct PagedWarp {
           const int kp = pos[nt * 8 + 2 * t4 + c];
 #pragma unroll
           for (int r = 0; r < NR; ++r)
-            if (kp > row_pos[r]) sc[nt][2 * r + c] = -INFINITY;
+            if (MULTI ? kp > row_pos[r] : kp == kPagedNone) sc[nt][2 * r + c] = -INFINITY;
         }
     }
 
@@ -360,13 +367,13 @@ struct PagedWarp {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float m_new = fmaxf(m_run[r], mx * sl2);
       const float mu = m_new == -INFINITY ? 0.f : m_new;  // no visible key yet
-      alpha[r] = exp2f(m_run[r] - mu);                     // 0 while m_run is -inf
+      alpha[r] = dec_exp2(m_run[r] - mu);                  // 0 while m_run is -inf
       m_run[r] = m_new;
       float ls = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NS; ++nt) {
-        const float p0 = exp2f(fmaf(sc[nt][2 * r], sl2, -mu));
-        const float p1 = exp2f(fmaf(sc[nt][2 * r + 1], sl2, -mu));
+        const float p0 = dec_exp2(fmaf(sc[nt][2 * r], sl2, -mu));
+        const float p1 = dec_exp2(fmaf(sc[nt][2 * r + 1], sl2, -mu));
         ls += p0 + p1;
         sc[nt][2 * r] = p0;
         sc[nt][2 * r + 1] = p1;
@@ -375,19 +382,20 @@ struct PagedWarp {
       }
       l_run[r] = fmaf(l_run[r], alpha[r], ls);
     }
+    // (where no row's maximum moved, there is nothing to rescale)
+    if (dec_ballot(alpha[0] != 1.f || (UP && alpha[NR - 1] != 1.f)) != 0u) {
 #pragma unroll
-    for (int j = 0; j < NO; ++j) {
-      o[j][0] *= alpha[0];
-      o[j][1] *= alpha[0];
-      if constexpr (UP) {
-        o[j][2] *= alpha[1];
-        o[j][3] *= alpha[1];
+      for (int j = 0; j < NO; ++j) {
+        o[j][0] *= alpha[0];
+        o[j][1] *= alpha[0];
+        o[j][2] *= alpha[NR - 1];  // without UP: the lo half of row g
+        o[j][3] *= alpha[NR - 1];
       }
     }
     // A key that some rows see and others do not: its value must not touch
     // those others, not even as 0 * NaN.  Its products are done one by one,
     // and its row of V is cleared for the matrix product below.
-    if (masked && p.Tq > 1) {
+    if (MULTI && masked) {
       for (int key = 0; key < CK; ++key) {
         const int kp = pos[key];
         if (kp <= pos0 || kp == kPagedNone) continue;
@@ -427,14 +435,23 @@ struct PagedWarp {
         const int mi = lane >> 3;
         uint32_t r[4];
         dec_ldsm_x4_t(r, sv + dec_swz<D>(kk * 16 + (mi & 1) * 8 + (lane & 7), 2 * jj + (mi >> 1)));
-        const uint32_t h1 = UP ? hi[2 * kk][NR - 1] : 0u, h3 = UP ? hi[2 * kk + 1][NR - 1] : 0u;
-        const uint32_t l1 = UP ? lo[2 * kk][NR - 1] : 0u, l3 = UP ? lo[2 * kk + 1][NR - 1] : 0u;
-        dec_mma(o[2 * jj], hi[2 * kk][0], h1, hi[2 * kk + 1][0], h3, r[0], r[1]);
-        dec_mma(o[2 * jj + 1], hi[2 * kk][0], h1, hi[2 * kk + 1][0], h3, r[2], r[3]);
-        dec_mma(o[2 * jj], lo[2 * kk][0], l1, lo[2 * kk + 1][0], l3, r[0], r[1]);
-        dec_mma(o[2 * jj + 1], lo[2 * kk][0], l1, lo[2 * kk + 1][0], l3, r[2], r[3]);
+        const uint32_t b1 = UP ? hi[2 * kk][NR - 1] : lo[2 * kk][0];
+        const uint32_t b3 = UP ? hi[2 * kk + 1][NR - 1] : lo[2 * kk + 1][0];
+        dec_mma(o[2 * jj], hi[2 * kk][0], b1, hi[2 * kk + 1][0], b3, r[0], r[1]);
+        dec_mma(o[2 * jj + 1], hi[2 * kk][0], b1, hi[2 * kk + 1][0], b3, r[2], r[3]);
+        if constexpr (UP) {
+          dec_mma(o[2 * jj], lo[2 * kk][0], lo[2 * kk][1], lo[2 * kk + 1][0], lo[2 * kk + 1][1],
+                  r[0], r[1]);
+          dec_mma(o[2 * jj + 1], lo[2 * kk][0], lo[2 * kk][1], lo[2 * kk + 1][0],
+                  lo[2 * kk + 1][1], r[2], r[3]);
+        }
       }
     }
+  }
+
+  // Column pair c of row r of n-tile j.
+  __device__ __forceinline__ float out(int j, int r, int c) const {
+    return UP ? o[j][2 * r + c] : o[j][c] + o[j][2 + c];
   }
 
   // Row r's sum over the quad that shares it.
@@ -459,7 +476,7 @@ struct PagedWarp {
 #pragma unroll
       for (int j = 0; j < NO; ++j)
         *reinterpret_cast<uint32_t*>(ob + 8 * j + 2 * t4) =
-            dec_pack_bf16(o[j][2 * r] * inv, o[j][2 * r + 1] * inv);
+            dec_pack_bf16(out(j, r, 0) * inv, out(j, r, 1) * inv);
       if (t4 == 0)
         p.lse[(x.b * static_cast<long long>(p.H) + hq) * p.Tq + t] = paged_lse(m_run[r], l);
     }
@@ -476,7 +493,7 @@ struct PagedWarp {
 #pragma unroll
       for (int j = 0; j < NO; ++j)
         *reinterpret_cast<float2*>(ov + row * D + 8 * j + 2 * t4) =
-            float2{o[j][2 * r], o[j][2 * r + 1]};
+            float2{out(j, r, 0), out(j, r, 1)};
     }
   }
 };
@@ -540,7 +557,7 @@ __device__ __forceinline__ void paged_write(const PagedParams& p, const PagedPla
 // results are joined in shared memory, the CTAs' in distributed shared memory.
 // Nothing to scan, no workspace, one launch.  Grid: items * ctas in clusters of
 // ctas.
-template <int D, bool UP>
+template <int D, bool UP, bool MULTI>
 __global__ void __launch_bounds__(kPagedThreads, 2)
     paged_item_kernel(const PagedParams p, int ctas) {
   dec_grid_dep_wait();
@@ -557,9 +574,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   x.c = rank * kPagedWarps + warp;
   const int step = ctas * kPagedWarps, h = x.ht / p.n_tiles;
   const int left = x.n > x.c ? (x.n - x.c + step - 1) / step : 0;
-  PagedWarp<D, UP> k(p, smem, warp, lane);
+  PagedWarp<D, UP, MULTI> k(p, smem, warp, lane);
   // the first chunks' keys are looked up together, then one ahead
-  PagedKey key[kPagedStages], next{-1, 0, kPagedNone};
+  PagedKey key[kPagedStages], next{-1, -1, kPagedNone};
   auto look_up = [&](int i) {
     PagedPlace y = x;
     y.c = x.c + i * step;
@@ -591,7 +608,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   dec_cp_async_wait<0>();
   const PagedMerge a = paged_merge_area<D>(smem);
   __syncthreads();  // every warp is done with its ring
-  k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, kPagedRows);
+  k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, p.R);
   __syncthreads();
   const int r0 = (x.ht - h * p.n_tiles) * kPagedRows;
   const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;
@@ -627,7 +644,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 // A CTA takes an even share of the flat axis.  If all of it lies in one item
 // the warps take turns at its chunks and join their results in shared
 // memory; otherwise each takes a quarter of the share.
-template <int D, bool UP>
+template <int D, bool UP, bool MULTI>
 __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const PagedParams p) {
   dec_grid_dep_wait();
   dec_grid_dep_launch();
@@ -689,10 +706,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     return static_cast<int>(c * kPagedWarps + w - gw) + 1;
   };
 
-  PagedWarp<D, UP> k(p, smem, warp, lane);
+  PagedWarp<D, UP, MULTI> k(p, smem, warp, lane);
   PagedPlace get = use;
   int to_look = left;
-  PagedKey key[kPagedStages], next{-1, 0, kPagedNone};
+  PagedKey key[kPagedStages], next{-1, -1, kPagedNone};
   int hts[kPagedStages];
   auto look_up = [&](PagedKey& to) {  // the next chunk's keys, and on to the one behind it
     to = k.look_up(get);
@@ -763,7 +780,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     const bool whole = first.c == 0 && share == first.n;
     const PagedMerge a = paged_merge_area<D>(smem);
     __syncthreads();  // every warp is done with its ring
-    k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, kPagedRows);
+    k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, p.R);
     __syncthreads();
     const int h = first.ht / p.n_tiles, r0 = (first.ht - h * p.n_tiles) * kPagedRows;
     const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;

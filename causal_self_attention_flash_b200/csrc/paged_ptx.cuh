@@ -30,6 +30,12 @@ __device__ __forceinline__ int dec_lowest(unsigned x) { return __ffs(static_cast
 __device__ __forceinline__ long long dec_double_bits(double x) { return __double_as_longlong(x); }
 __device__ __forceinline__ unsigned dec_float_bits(float x) { return __float_as_uint(x); }
 __device__ __forceinline__ float dec_bits_float(unsigned u) { return __uint_as_float(u); }
+// 2^x to 2 ulp; results below the smallest normal number are 0.
+__device__ __forceinline__ float dec_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
 // Sum over the warp's lanes.
 __device__ __forceinline__ int dec_warp_sum(int v) { return __reduce_add_sync(kFullWarp, v); }
 __device__ __forceinline__ unsigned dec_warp_min(unsigned v) {

@@ -53,18 +53,28 @@ static void put(const void* p, size_t bytes) {
   if (bytes) std::fwrite(p, 1, bytes, g_out);
 }
 
-template <int D, bool UP>
-static void run_decode(const PagedParams& p, int grid) {
+template <int D, bool UP, bool MULTI>
+static void run_decode_as(const PagedParams& p, int grid) {
   if (grid < 0) {
     emu::launch_ex(static_cast<unsigned>(p.B * p.Hkv * p.n_tiles * -grid), kPagedThreads,
-                   paged_smem_bytes(D), static_cast<unsigned>(-grid), paged_item_kernel<D, UP>, p,
-                   -grid);
+                   paged_smem_bytes(D), static_cast<unsigned>(-grid), paged_item_kernel<D, UP, MULTI>,
+                   p, -grid);
     return;
   }
-  emu::launch_ex(grid, kPagedThreads, paged_smem_bytes(D), 1, paged_decode_kernel<D, UP>, p);
+  emu::launch_ex(grid, kPagedThreads, paged_smem_bytes(D), 1, paged_decode_kernel<D, UP, MULTI>,
+                 p);
   const int n_y = paged_merge_y(p.R);
   emu::launch_ex(grid * n_y, kMergeThreads, paged_merge_smem_bytes(D), 1, paged_merge_kernel<D>,
                  p, n_y);
+}
+
+template <int D>
+static void run_decode(const PagedParams& p, int grid) {
+  const bool up = p.rows > 8, multi = p.Tq > 1;
+  if (up)
+    multi ? run_decode_as<D, true, true>(p, grid) : run_decode_as<D, true, false>(p, grid);
+  else
+    multi ? run_decode_as<D, false, true>(p, grid) : run_decode_as<D, false, false>(p, grid);
 }
 
 // params: B H Hkv Tq D n_pages P width n_sel grid layout (grid < 0: -grid CTAs
@@ -104,12 +114,11 @@ static void decode() {
   p.cuts = out<PagedCut>(warps);
   p.part_ml = out<float2>(2 * warps * p.R);
   p.part_o = out<float>(2 * warps * p.R * D);
-  const bool up = p.rows > 8;
   switch (D) {
-    case 16: up ? run_decode<16, true>(p, grid) : run_decode<16, false>(p, grid); break;
-    case 32: up ? run_decode<32, true>(p, grid) : run_decode<32, false>(p, grid); break;
-    case 64: up ? run_decode<64, true>(p, grid) : run_decode<64, false>(p, grid); break;
-    case 128: up ? run_decode<128, true>(p, grid) : run_decode<128, false>(p, grid); break;
+    case 16: run_decode<16>(p, grid); break;
+    case 32: run_decode<32>(p, grid); break;
+    case 64: run_decode<64>(p, grid); break;
+    case 128: run_decode<128>(p, grid); break;
     default: std::exit(4);
   }
   put(p.o, rows * D * 2);

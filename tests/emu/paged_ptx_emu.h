@@ -81,6 +81,10 @@ inline long long dec_double_bits(double x) {
   std::memcpy(&r, &x, 8);
   return r;
 }
+inline float dec_exp2(float x) {
+  const float y = std::exp2(x);
+  return y < 0x1p-126f ? 0.f : y;
+}
 inline unsigned dec_cluster_rank() { return emu::t_cta->rank; }
 inline uint32_t dec_bf16_absmax(uint32_t m, uint32_t x) {
   x &= 0x7fff7fffu;
