@@ -482,8 +482,9 @@ struct PagedWarp {
     }
   }
 
-  // The state as rows [r] of ml (m, l) and of ov (o), R of them.
-  __device__ __forceinline__ void store(float2* ml, float* ov, int R) {
+  // The state as rows [r] of ml (m, l) and of ov (o, `pitch` floats apart), R of
+  // them.
+  __device__ __forceinline__ void store(float2* ml, float* ov, int R, int pitch) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const float l = row_sum(r);
@@ -492,28 +493,76 @@ struct PagedWarp {
       if (t4 == 0) ml[row] = float2{m_run[r], l};
 #pragma unroll
       for (int j = 0; j < NO; ++j)
-        *reinterpret_cast<float2*>(ov + row * D + 8 * j + 2 * t4) =
+        *reinterpret_cast<float2*>(ov + row * pitch + 8 * j + 2 * t4) =
             float2{out(j, r, 0), out(j, r, 1)};
     }
   }
 };
 
 // Shared memory of a CTA's merge, over the rings: (m, l) and o of each warp,
-// then the CTA's own.
+// then the CTA's own.  Rows of o are 8 floats longer than D, so that the eight
+// rows of a fragment fall into different banks.
+template <int D>
 struct PagedMerge {
+  static constexpr int PITCH = D + 8;
+  static_assert((kPagedWarps + 1) * kPagedRows * (PITCH + 2) * 4 <= paged_ring_bytes(D),
+                "merge area");
   float2 *ml, *cta_ml;
   float *ov, *cta_ov;
+  __device__ __forceinline__ explicit PagedMerge(uint8_t* smem) {
+    ml = reinterpret_cast<float2*>(smem);
+    cta_ml = ml + kPagedWarps * kPagedRows;
+    ov = reinterpret_cast<float*>(cta_ml + kPagedRows);
+    cta_ov = ov + kPagedWarps * kPagedRows * PITCH;
+  }
+  // Row r's column d over n parts (m, l, o): M, L and the sum.  A part without
+  // keys has l = 0; l = NaN goes on whatever its m.
+  template <int N>
+  static __device__ __forceinline__ float sum(const float2 (&part)[N], const float (&o)[N],
+                                              float& M, float& L) {
+    M = part[0].x;
+#pragma unroll
+    for (int i = 1; i < N; ++i) M = fmaxf(M, part[i].x);
+    const float mu = M == -INFINITY ? 0.f : M;
+    float acc = 0.f;
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float f =
+          part[i].x == -INFINITY ? (part[i].y == 0.f ? 0.f : 1.f) : dec_exp2(part[i].x - mu);
+      L = fmaf(f, part[i].y, L);
+      acc = fmaf(f, o[i], acc);
+    }
+    return acc;
+  }
+  // Over the CTA's warps.
+  __device__ __forceinline__ float warps(int r, int d, float& M, float& L) const {
+    float2 part[kPagedWarps];
+    float o[kPagedWarps];
+#pragma unroll
+    for (int w = 0; w < kPagedWarps; ++w) {
+      part[w] = ml[w * kPagedRows + r];
+      o[w] = ov[(w * kPagedRows + r) * PITCH + d];
+    }
+    return sum(part, o, M, L);
+  }
+  // Over the cluster's CTAs.
+  __device__ __forceinline__ float ctas(int n, int r, int d, float& M, float& L) const {
+    float2 part[8];
+    float o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      part[c] = float2{-INFINITY, 0.f};
+      o[c] = 0.f;
+      if (c < n) {
+        part[c].x = dec_cluster_ld(&cta_ml[r].x, c);
+        part[c].y = dec_cluster_ld(&cta_ml[r].y, c);
+        o[c] = dec_cluster_ld(cta_ov + r * PITCH + d, c);
+      }
+    }
+    return sum(part, o, M, L);
+  }
 };
-template <int D>
-__device__ __forceinline__ PagedMerge paged_merge_area(uint8_t* smem) {
-  static_assert((kPagedWarps + 1) * kPagedRows * (D + 2) * 4 <= paged_ring_bytes(D), "merge area");
-  PagedMerge a;
-  a.ml = reinterpret_cast<float2*>(smem);
-  a.cta_ml = a.ml + kPagedWarps * kPagedRows;
-  a.ov = reinterpret_cast<float*>(a.cta_ml + kPagedRows);
-  a.cta_ov = a.ov + kPagedWarps * kPagedRows * D;
-  return a;
-}
 
 // One more part (m, l) for a running (M, L): the factors of the two.  A part
 // without keys has l = 0; l = NaN goes on whatever its m.
@@ -524,22 +573,6 @@ __device__ __forceinline__ void paged_join(float m, float l, float& M, float& L,
   fb = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - mu);
   M = m_new;
   L = fmaf(L, fa, fb * l);
-}
-
-// Row r's column d over the CTA's warps, from the merge area: M, L and the sum.
-template <int D>
-__device__ __forceinline__ float paged_cta_sum(const PagedMerge& a, int r, int d, float& M,
-                                               float& L) {
-  float acc = 0.f, fa, fb;
-  M = -INFINITY;
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kPagedWarps; ++w) {
-    const float2 ml = a.ml[w * kPagedRows + r];
-    paged_join(ml.x, ml.y, M, L, fa, fb);
-    acc = fmaf(acc, fa, fb * a.ov[(w * kPagedRows + r) * D + d]);
-  }
-  return acc;
 }
 
 // o and lse of row r (of tile r0), column d of item x.
@@ -606,20 +639,20 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     slot = slot + 1 == kPagedStages ? 0 : slot + 1;
   }
   dec_cp_async_wait<0>();
-  const PagedMerge a = paged_merge_area<D>(smem);
+  const PagedMerge<D> a(smem);
   __syncthreads();  // every warp is done with its ring
-  k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, p.R);
+  k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * a.PITCH, p.R, a.PITCH);
   __syncthreads();
   const int r0 = (x.ht - h * p.n_tiles) * kPagedRows;
   const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;
   for (int i = tid; i < rows * D; i += kPagedThreads) {
     const int r = i / D, d = i - r * D;
     float M, L;
-    const float acc = paged_cta_sum<D>(a, r, d, M, L);
+    const float acc = a.warps(r, d, M, L);
     if (ctas == 1) {
       paged_write(p, x, h, r0 + r, d, M, L, acc);
     } else {
-      a.cta_ov[i] = acc;
+      a.cta_ov[r * a.PITCH + d] = acc;
       if (d == 0) a.cta_ml[r] = float2{M, L};
     }
   }
@@ -627,12 +660,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   dec_cluster_sync();  // every CTA's part is in its shared memory
   for (int i = rank * kPagedThreads + tid; i < rows * D; i += ctas * kPagedThreads) {
     const int r = i / D, d = i - r * D;
-    float M = -INFINITY, L = 0.f, acc = 0.f, fa, fb;
-    for (int c = 0; c < ctas; ++c) {
-      const float m = dec_cluster_ld(&a.cta_ml[r].x, c), l = dec_cluster_ld(&a.cta_ml[r].y, c);
-      paged_join(m, l, M, L, fa, fb);
-      acc = fmaf(acc, fa, fb * dec_cluster_ld(a.cta_ov + i, c));
-    }
+    float M, L;
+    const float acc = a.ctas(ctas, r, d, M, L);
     paged_write(p, x, h, r0 + r, d, M, L, acc);
   }
   dec_cluster_sync();  // no CTA leaves while its shared memory is read
@@ -762,7 +791,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
         k.finish(use);
       } else {
         const long long part = (2LL * gw + begins) * p.R;
-        k.store(p.part_ml + part, p.part_o + part * D, p.R);
+        k.store(p.part_ml + part, p.part_o + part * D, p.R, D);
       }
       if (begins && !ends)  // cut here: the warps that hold its other chunks
         cut = PagedCut{use.b, use.ht,
@@ -778,9 +807,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
 
   if (together) {
     const bool whole = first.c == 0 && share == first.n;
-    const PagedMerge a = paged_merge_area<D>(smem);
+    const PagedMerge<D> a(smem);
     __syncthreads();  // every warp is done with its ring
-    k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * D, p.R);
+    k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * a.PITCH, p.R, a.PITCH);
     __syncthreads();
     const int h = first.ht / p.n_tiles, r0 = (first.ht - h * p.n_tiles) * kPagedRows;
     const int rows = p.rows - r0 < kPagedRows ? p.rows - r0 : kPagedRows;
@@ -788,7 +817,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     for (int i = tid; i < rows * D && first.b < p.B; i += kPagedThreads) {
       const int r = i / D, d = i - r * D;
       float M, L;
-      const float acc = paged_cta_sum<D>(a, r, d, M, L);
+      const float acc = a.warps(r, d, M, L);
       if (whole) {
         paged_write(p, first, h, r0 + r, d, M, L, acc);
       } else {
