@@ -766,19 +766,20 @@ cattn_status paged_impl(const PagedParams& p, int ctas, int grid, int dev, cudaS
   const auto flat_kernel = paged_decode_kernel<D, UP, MULTI>;
   const auto item_kernel = paged_item_kernel<D, UP, MULTI>;
   const unsigned bit = 87 + 4 * d_index(D) + 2 * UP + MULTI;
-  cattn_status st = item ? ensure_smem(dev, bit, item_kernel, paged_smem_bytes(D))
-                         : ensure_smem(dev, bit + 16, flat_kernel, paged_smem_bytes(D));
+  cattn_status st = item ? ensure_smem(dev, bit, item_kernel, paged_smem_bytes(D, kItemStages))
+                         : ensure_smem(dev, bit + 16, flat_kernel,
+                                       paged_smem_bytes(D, kPagedStages));
   if (st != CATTN_OK) return st;
   clear_stale_error();
   LaunchTimer t(K_DECODE, s);
   const long long items = static_cast<long long>(p.B) * p.Hkv * p.n_tiles;
   cudaError_t e = cudaSuccess;
   if (item) {
-    e = launch_cluster(item_kernel, items * ctas, kPagedThreads, ctas, paged_smem_bytes(D), s, p,
-                       ctas);
+    e = launch_cluster(item_kernel, items * ctas, kPagedThreads, ctas,
+                       paged_smem_bytes(D, kItemStages), s, p, ctas);
   } else {
-    e = launch_dependent(true, flat_kernel, dim3(grid), dim3(kPagedThreads), paged_smem_bytes(D),
-                         s, p);
+    e = launch_dependent(true, flat_kernel, dim3(grid), dim3(kPagedThreads),
+                         paged_smem_bytes(D, kPagedStages), s, p);
     if (e == cudaSuccess)
       e = launch_dependent(true, paged_merge_kernel<D>, dim3(grid * paged_merge_y(p.R)),
                            dim3(kMergeThreads), paged_merge_smem_bytes(D), s, p,
@@ -848,6 +849,7 @@ cattn_status paged_decode(const void* q, cattn_layout lq, const void* k, cattn_l
   p.B = B; p.H = H; p.Hkv = Hkv; p.Tq = Tq;
   p.n_pages = n_pages; p.P = P; p.width = width; p.n_sel = n_sel;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.by_P = PageDivider(P);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.cuts = reinterpret_cast<PagedCut*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + paged_ml_offset());
@@ -1153,7 +1155,7 @@ cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t* lengths,
   p.slots = reinterpret_cast<long long*>(slots);
   p.positions = positions;
   p.status = status;
-  plan_divider(p);
+  p.by_P = PageDivider(page_size);
   const int n = plan_ctas(n_slots, B);
   clear_stale_error();
   cudaStream_t s = static_cast<cudaStream_t>(stream);

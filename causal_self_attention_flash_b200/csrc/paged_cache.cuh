@@ -49,21 +49,8 @@ struct PlanParams {
   long long* slots;            // (n_slots)
   int* positions;              // (n_slots)
   int* status;                 // (1)
-  // n / P for 0 <= n <= 2^30 as (n mul) >> shift: with shift = 31 + L, 2^L >= P,
-  // and mul = floor(2^shift / P) + 1 <= 2^32, n mul / 2^shift exceeds n / P by at most
-  // n / 2^shift <= 1 / (2 P), too little to reach the next whole number.
-  unsigned long long mul;
-  int shift;
-  __host__ __device__ int by_P(int n) const {
-    return static_cast<int>((static_cast<unsigned long long>(n) * mul) >> shift);
-  }
+  PageDivider by_P;
 };
-__host__ __device__ inline void plan_divider(PlanParams& p) {
-  int L = 0;
-  while ((1LL << L) < p.P) ++L;
-  p.shift = 31 + L;
-  p.mul = (1ull << p.shift) / static_cast<unsigned>(p.P) + 1;
-}
 
 __host__ __device__ constexpr int plan_smem_bytes(int B) {
   return 16 * (B + 1) + kPlanThreads / 32 * 32 + 16;  // prefix sums, warp totals, faults

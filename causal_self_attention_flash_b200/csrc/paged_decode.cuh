@@ -45,7 +45,9 @@ namespace cattn {
 constexpr int kPagedWarps = 4;                    // warps per CTA
 constexpr int kPagedThreads = 32 * kPagedWarps;
 constexpr int kPagedStages = 3;                   // chunks in flight per warp
+constexpr int kItemStages = 2;                    // in paged_item_kernel
 constexpr int kPagedMaxCtas = 2 * 148;            // resident CTAs of a B200 (2 x 99 KB)
+constexpr int kItemSlots = 3 * 148;               // resident CTAs of paged_item_kernel (66 KB)
 constexpr int kPagedMaxWarps = kPagedMaxCtas * kPagedWarps;
 constexpr int kPagedMinRun = 2;                   // chunks that a warp takes at least
 constexpr int kPagedRows = 16;                    // query rows per item
@@ -56,13 +58,13 @@ constexpr int kMergeThreads = 256;
 // per key.
 __host__ __device__ constexpr int paged_chunk(int D) { return D == 128 ? 16 : 32; }
 __host__ __device__ constexpr int paged_chunk_bytes(int D) { return paged_chunk(D) * D * 4; }
-__host__ __device__ constexpr int paged_ring_bytes(int D) {
-  return kPagedWarps * kPagedStages * paged_chunk_bytes(D);
+__host__ __device__ constexpr int paged_ring_bytes(int D, int stages) {
+  return kPagedWarps * stages * paged_chunk_bytes(D);
 }
 // Dynamic shared memory: the rings, the key positions of their slots, the
 // scan's prefix sums and warp totals.
-__host__ __device__ constexpr int paged_smem_bytes(int D) {
-  return paged_ring_bytes(D) + kPagedWarps * kPagedStages * 32 * 4 + (kPagedThreads + 8) * 4;
+__host__ __device__ constexpr int paged_smem_bytes(int D, int stages) {
+  return paged_ring_bytes(D, stages) + kPagedWarps * stages * 32 * 4 + (kPagedThreads + 8) * 4;
 }
 
 // Where a cut item begins: its partial results are slot 1 of warp w and
@@ -83,6 +85,23 @@ __host__ __device__ constexpr long long paged_workspace_bytes(int R, int D) {
   return paged_o_offset(R) + 2LL * kPagedMaxWarps * R * D * 4;
 }
 
+// n / P for 0 <= n <= 2^30 as (n mul) >> shift: with shift = 31 + L, 2^L >= P,
+// and mul = floor(2^shift / P) + 1 <= 2^32, n mul / 2^shift exceeds n / P by at
+// most n / 2^shift <= 1 / (2 P), too little to reach the next whole number.
+struct PageDivider {
+  unsigned long long mul;
+  int shift;
+  __host__ __device__ explicit PageDivider(int P = 1) {
+    int L = 0;
+    while ((1LL << L) < P) ++L;
+    shift = 31 + L;
+    mul = (1ull << shift) / static_cast<unsigned>(P) + 1;
+  }
+  __host__ __device__ int operator()(int n) const {
+    return static_cast<int>((static_cast<unsigned long long>(n) * mul) >> shift);
+  }
+};
+
 struct PagedParams {
   const __nv_bfloat16* q;  // (B, H, Tq, D)
   const __nv_bfloat16* k;  // (n_pages, Hkv, P, D)
@@ -100,6 +119,7 @@ struct PagedParams {
   int n_pages, P, width, n_sel;
   int R;                   // rows of a partial slot, min(16, rows)
   float scale_log2;        // scale * log2(e)
+  PageDivider by_P;
   PagedCut* cuts;
   float2* part_ml;         // [2 warps][R]
   float* part_o;           // [2 warps][R][D]
@@ -109,10 +129,8 @@ struct PagedParams {
 // and the chunks they take; an item without keys has one, empty, chunk.
 __device__ __forceinline__ int paged_keys(const PagedParams& p, int len) {
   if (len < 0) len = 0;
-  if (p.pages != nullptr) {
-    const int have = len / p.P + (len % p.P != 0);
-    return (have < p.n_sel ? have : p.n_sel) * p.P;
-  }
+  if (p.pages != nullptr)  // (a list holds at most 2^30 keys)
+    return len >= p.n_sel * p.P ? p.n_sel * p.P : (p.by_P(len + p.P - 1)) * p.P;
   const int cap = p.width * p.P;
   return len < cap ? len : cap;
 }
@@ -200,7 +218,7 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
 // One warp's work on chunks: its ring of shared memory slots and the running
 // state of the item it is in.  UP: rows 8 .. 15 of the tile are used.  MULTI:
 // several new positions (Tq > 1), so that rows may see different keys.
-template <int D, bool UP, bool MULTI>
+template <int D, bool UP, bool MULTI, int STAGES>
 struct PagedWarp {
   static constexpr int CK = paged_chunk(D);  // keys per chunk
   static constexpr int PC = D / 8;           // 16-byte pieces per row
@@ -226,8 +244,8 @@ struct PagedWarp {
                                        int lane_)
       : p(params), lane(lane_), g(lane_ >> 2), t4(lane_ & 3),
         same(params.k_sp == params.v_sp && params.k_st == params.v_st) {
-    ring = smem + warp * (kPagedStages * CB);
-    slot_pos = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + warp * kPagedStages * 32;
+    ring = smem + warp * (STAGES * CB);
+    slot_pos = reinterpret_cast<int*>(smem + paged_ring_bytes(D, STAGES)) + warp * STAGES * 32;
     clear();
   }
 
@@ -245,14 +263,13 @@ struct PagedWarp {
   __device__ __forceinline__ PagedKey look_up(const PagedPlace& x) const {
     PagedKey key{-1, -1, kPagedNone};
     const int vk = x.c * CK + lane;
-    const int li = vk / p.P;
+    const int li = p.by_P(vk);
     const int row = vk - li * p.P;
     int lp = -1;
     if (lane < CK && x.b < p.B) {
       if (p.pages != nullptr) {
         const int h = x.ht / p.n_tiles;
-        const int have = paged_keys(p, x.len) / p.P;
-        if (li < have) lp = p.pages[(static_cast<long long>(x.b) * p.Hkv + h) * p.n_sel + li];
+        if (vk < paged_keys(p, x.len)) lp = p.pages[(static_cast<long long>(x.b) * p.Hkv + h) * p.n_sel + li];
       } else {
         lp = li;
       }
@@ -505,8 +522,8 @@ struct PagedWarp {
 template <int D>
 struct PagedMerge {
   static constexpr int PITCH = D + 8;
-  static_assert((kPagedWarps + 1) * kPagedRows * (PITCH + 2) * 4 <= paged_ring_bytes(D),
-                "merge area");
+  static_assert((kPagedWarps + 1) * kPagedRows * (PITCH + 2) * 4 <=
+                    paged_ring_bytes(D, kItemStages), "merge area");
   float2 *ml, *cta_ml;
   float *ov, *cta_ov;
   __device__ __forceinline__ explicit PagedMerge(uint8_t* smem) {
@@ -591,7 +608,7 @@ __device__ __forceinline__ void paged_write(const PagedParams& p, const PagedPla
 // Nothing to scan, no workspace, one launch.  Grid: items * ctas in clusters of
 // ctas.
 template <int D, bool UP, bool MULTI>
-__global__ void __launch_bounds__(kPagedThreads, 2)
+__global__ void __launch_bounds__(kPagedThreads, UP && D == 128 ? 2 : 3)
     paged_item_kernel(const PagedParams p, int ctas) {
   dec_grid_dep_wait();
   dec_grid_dep_launch();
@@ -607,36 +624,36 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   x.c = rank * kPagedWarps + warp;
   const int step = ctas * kPagedWarps, h = x.ht / p.n_tiles;
   const int left = x.n > x.c ? (x.n - x.c + step - 1) / step : 0;
-  PagedWarp<D, UP, MULTI> k(p, smem, warp, lane);
+  PagedWarp<D, UP, MULTI, kItemStages> k(p, smem, warp, lane);
   // the first chunks' keys are looked up together, then one ahead
-  PagedKey key[kPagedStages], next{-1, -1, kPagedNone};
+  PagedKey key[kItemStages], next{-1, -1, kPagedNone};
   auto look_up = [&](int i) {
     PagedPlace y = x;
     y.c = x.c + i * step;
     return k.look_up(y);
   };
 #pragma unroll
-  for (int i = 0; i < kPagedStages; ++i)
+  for (int i = 0; i < kItemStages; ++i)
     if (i < left) key[i] = look_up(i);
 #pragma unroll
-  for (int i = 0; i < kPagedStages; ++i) {
+  for (int i = 0; i < kItemStages; ++i) {
     if (i < left) k.issue(x.ht, key[i], i);
     dec_cp_async_commit();
   }
-  if (kPagedStages < left) next = look_up(kPagedStages);
+  if (kItemStages < left) next = look_up(kItemStages);
   k.begin(x);
   int slot = 0;
   for (int i = 0; i < left; ++i) {
-    dec_cp_async_wait<kPagedStages - 1>();
+    dec_cp_async_wait<kItemStages - 1>();
     __syncwarp();  // every lane's pieces of the chunk are in shared memory
     k.chunk(slot, x.len);
     __syncwarp();  // every lane has read the slot: refill it
-    if (i + kPagedStages < left) {
+    if (i + kItemStages < left) {
       k.issue(x.ht, next, slot);
-      if (i + kPagedStages + 1 < left) next = look_up(i + kPagedStages + 1);
+      if (i + kItemStages + 1 < left) next = look_up(i + kItemStages + 1);
     }
     dec_cp_async_commit();
-    slot = slot + 1 == kPagedStages ? 0 : slot + 1;
+    slot = slot + 1 == kItemStages ? 0 : slot + 1;
   }
   dec_cp_async_wait<0>();
   const PagedMerge<D> a(smem);
@@ -667,8 +684,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   dec_cluster_sync();  // no CTA leaves while its shared memory is read
 }
 
-// Grid: up to kPagedMaxCtas CTAs of kPagedThreads, paged_smem_bytes(D) of
-// dynamic shared memory.
+// Grid: up to kPagedMaxCtas CTAs of kPagedThreads.
 //
 // A CTA takes an even share of the flat axis.  If all of it lies in one item
 // the warps take turns at its chunks and join their results in shared
@@ -679,7 +695,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
   dec_grid_dep_launch();
   uint8_t* smem = dec_dynamic_smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D)) + kPagedWarps * kPagedStages * 32;
+  int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D, kPagedStages)) + kPagedWarps * kPagedStages * 32;
   int* totals = pre + kPagedThreads;
   const int HT = p.Hkv * p.n_tiles;
 
@@ -735,7 +751,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     return static_cast<int>(c * kPagedWarps + w - gw) + 1;
   };
 
-  PagedWarp<D, UP, MULTI> k(p, smem, warp, lane);
+  PagedWarp<D, UP, MULTI, kPagedStages> k(p, smem, warp, lane);
   PagedPlace get = use;
   int to_look = left;
   PagedKey key[kPagedStages], next{-1, -1, kPagedNone};
@@ -836,12 +852,15 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
 
 // CTAs per item of paged_item_kernel, or 0 for paged_decode_kernel, from the
 // items and the chunks that the table (the list) has room for; the lengths are
-// not known here.
+// not known here.  As many CTAs as are resident at once; then the item kernel
+// where no warp has more than 9 chunks (16 x 12 heads x 1,024 keys of 64: 14.4
+// against 21.6 us for the other kernel; 4 x 8 x 2,048 of 128: 13.5, 18.3), the
+// other one for longer items, whose lengths may differ more (32 x 8 x 100 to
+// 1,000 keys of 128: 28.1, 23.6; 2 x 16 x 8,192: 35.3, 34.4).
 __host__ __device__ constexpr int paged_item_ctas(long long items, long long chunks) {
   int ctas = 1;
-  while (ctas < 8 && 2 * ctas * items <= kPagedMaxCtas && chunks > 2 * kPagedWarps * ctas)
-    ctas *= 2;
-  return items * ctas <= 2 * kPagedMaxCtas && chunks <= 16LL * kPagedWarps * ctas ? ctas : 0;
+  while (ctas < 8 && 2 * ctas * items <= kItemSlots && chunks > kPagedWarps * ctas) ctas *= 2;
+  return items * ctas <= 2 * kItemSlots && chunks <= 9LL * kPagedWarps * ctas ? ctas : 0;
 }
 
 // Joins the parts of the cut items:  M = max m_i,

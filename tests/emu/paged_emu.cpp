@@ -57,11 +57,11 @@ template <int D, bool UP, bool MULTI>
 static void run_decode_as(const PagedParams& p, int grid) {
   if (grid < 0) {
     emu::launch_ex(static_cast<unsigned>(p.B * p.Hkv * p.n_tiles * -grid), kPagedThreads,
-                   paged_smem_bytes(D), static_cast<unsigned>(-grid), paged_item_kernel<D, UP, MULTI>,
+                   paged_smem_bytes(D, kItemStages), static_cast<unsigned>(-grid), paged_item_kernel<D, UP, MULTI>,
                    p, -grid);
     return;
   }
-  emu::launch_ex(grid, kPagedThreads, paged_smem_bytes(D), 1, paged_decode_kernel<D, UP, MULTI>,
+  emu::launch_ex(grid, kPagedThreads, paged_smem_bytes(D, kPagedStages), 1, paged_decode_kernel<D, UP, MULTI>,
                  p);
   const int n_y = paged_merge_y(p.R);
   emu::launch_ex(grid * n_y, kMergeThreads, paged_merge_smem_bytes(D), 1, paged_merge_kernel<D>,
@@ -99,6 +99,7 @@ static void decode() {
   p.lengths = in<int>(5);
   p.pages = in<int>(6);
   p.scale_log2 = *in<float>(7) * 1.4426950408889634f;
+  p.by_P = PageDivider(p.P);
   p.q_sb = static_cast<long long>(p.H) * p.Tq * D;
   p.q_sh = static_cast<long long>(p.Tq) * D;
   p.q_st = D;
@@ -145,7 +146,7 @@ static void plan() {
   p.slots = out<long long>(p.n_slots);
   p.positions = out<int>(p.n_slots);
   p.status = out<int>(1);
-  plan_divider(p);
+  p.by_P = PageDivider(p.P);
   emu::launch_ex(ctas, a[7], plan_smem_bytes(p.B), ctas,
                  a[8] ? paged_plan_kernel<false> : paged_plan_kernel<true>, p,
                  static_cast<int>(ctas));
