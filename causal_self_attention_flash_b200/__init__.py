@@ -23,7 +23,7 @@ import torch
 from ._binding import (CALL_CACHE_APPEND, CALL_DECODE_PAGED, CALL_DECODE_SPARSE, CALL_NAMES,
                        CALL_PAGE_SELECT, CALL_PAGED_PLAN, CALL_WORDS, ERR_CUDA, ERR_INVALID_ARG, ERR_TIMEOUT, ERR_TOO_LARGE,
                        ERR_UNSUPPORTED, LIB, LIB_PATH, NOALLOC_SCRATCH_BYTES, OK,
-                       CattnError, Dropout, Layout)
+                       CattnError, Dropout, Layout, TORCH_CALLS)
 
 __all__ = [
     "attn_fwd", "attn_bwd", "attn_fwd_ex", "attn_bwd_ex", "attn_bwd_preprocess",
@@ -463,9 +463,11 @@ def attn_decode(q, k, v, L, scale=None, o=None, lse=None, workspace=None, stream
     return o, lse
 
 
-# The paged calls.  A step of a server makes them once per layer, so what
-# they cost in Python counts: each looks at a tensor's attributes once and
-# hands its arguments over as one array (attn_paged_call).
+# The paged calls.  A step of a server makes them once per layer, so what they
+# cost in Python counts.  On the current stream and with the outputs given,
+# TORCH_CALLS reads the tensors and makes the call (1 us before the launch);
+# what it does not recognise (-1) goes the long way below, which says what is
+# wrong or makes the call itself (7 us).
 
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
 
@@ -523,6 +525,13 @@ def _scratch(ws, dev, need):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _done(which, st):
+    """Whether a call through TORCH_CALLS was made; raises its error."""
+    if st > 0:
+        _check(CALL_NAMES[which], st)
+    return st == 0
+
+
 def _call(which, *words):
     pack = CALL_WORDS[which]
     st = LIB.attn_paged_call(which, pack.pack(*words), pack.size // 8)
@@ -539,6 +548,10 @@ def attn_paged_plan(new_tokens, lengths, block_table, free_ring, ring_state, pag
     int64 (2).  Returns (lengths_out, ring_state_out, cu_new, slots,
     positions, status), all on the device; lengths_out and ring_state_out may
     be lengths and ring_state.  status is 0, or why nothing was changed."""
+    if stream is None and lengths_out is not None and _done(CALL_PAGED_PLAN, TORCH_CALLS.plan(
+            new_tokens, lengths, block_table, free_ring, ring_state, page_size, n_slots,
+            lengths_out, ring_state_out, cu_new, slots, positions, status)):
+        return lengths_out, ring_state_out, cu_new, slots, positions, status
     dev = _device(new_tokens)
     B, n_pages = new_tokens.numel(), free_ring.numel()
     if n_slots < 0:
@@ -565,6 +578,9 @@ def attn_cache_append(k_new, v_new, k_cache, v_cache, slots, bounds=None, stream
     bf16 (n_pages, Hkv, page_size, D) views.  bounds, bf16 (n_pages, Hkv, 2,
     D): the pages' lowest and highest key values, kept up to date for
     attn_page_select."""
+    if stream is None and _done(CALL_CACHE_APPEND, TORCH_CALLS.append(
+            k_new, v_new, k_cache, v_cache, slots, bounds)):
+        return
     dev = _device(k_new)
     cache = k_cache.shape
     if len(cache) != 4:
@@ -590,6 +606,9 @@ def attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D):
 
 def _decode_paged(which, q, k_cache, v_cache, block_table, lengths, pages, scale, o, lse,
                   workspace, stream):
+    if stream is None and o is not None and _done(which, TORCH_CALLS.decode(
+            q, k_cache, v_cache, block_table, lengths, pages, scale, o, lse, workspace)):
+        return o, lse
     dev = _device(q)
     shape, cache = q.shape, k_cache.shape
     if len(shape) != 4 or len(cache) != 4 or cache[3] != shape[3]:
@@ -651,6 +670,10 @@ def attn_page_select(q, bounds, block_table, lengths, page_size, n_select, n_fir
     (see attn_cache_append) promise the largest scores for the query rows q
     bf16 (B, H, Tq, D), the n_first first and n_last last among them; int32
     (B, Hkv, n_select), ascending, -1 behind the last."""
+    if stream is None and pages is not None and _done(CALL_PAGE_SELECT, TORCH_CALLS.select(
+            q, bounds, block_table, lengths, page_size, n_select, n_first, n_last, pages,
+            workspace)):
+        return pages
     dev = _device(q)
     shape, bs = q.shape, bounds.shape
     if len(shape) != 4 or len(bs) != 4:

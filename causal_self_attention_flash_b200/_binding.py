@@ -11,6 +11,8 @@ import ctypes
 import os
 import struct
 
+import torch  # noqa: F401  (before _torch_calls, which links against its libraries)
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcattn.so")
 
@@ -128,3 +130,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 LIB = load()
+
+
+def load_torch_calls():
+    """The marshalling of the paged calls (csrc/torch_calls.cpp), set to make
+    them through this process's libcattn."""
+    try:
+        from . import _torch_calls
+    except ImportError as e:
+        raise ImportError(
+            f"_torch_calls.so is missing or was built for another torch ({e}); build it with "
+            "`python causal_self_attention_flash_b200/build.py`") from e
+    _torch_calls.use(ctypes.cast(LIB.attn_paged_call, ctypes.c_void_p).value)
+    return _torch_calls
+
+
+TORCH_CALLS = load_torch_calls()

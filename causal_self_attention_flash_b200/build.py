@@ -1,8 +1,9 @@
-"""Build libcattn.so (sm_100a) in-tree with nvcc.
+"""Build libcattn.so (sm_100a) in-tree with nvcc, and _torch_calls.so, the
+Python binding's argument marshalling, with the host compiler.
 
     python causal_self_attention_flash_b200/build.py [--force]
 
-The library lands next to this file, so it travels with the source tree.
+Both land next to this file, so they travel with the source tree.
 """
 
 from __future__ import annotations
@@ -18,7 +19,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcattn.so")
 
+BINDING = os.path.join(HERE, "_torch_calls.so")
+
 SOURCES = ["api.cu"]
+BINDING_SOURCE = "torch_calls.cpp"
 # every device source and header: a change to any of them rebuilds
 DEPS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh")))
 
@@ -46,7 +50,33 @@ def _stale() -> bool:
     return any(os.path.getmtime(f) > t for f in files)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """_torch_calls.so, against the headers of the installed torch."""
+    src = os.path.join(CSRC, BINDING_SOURCE)
+    files = [src, os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in files):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    lib = os.path.join(root, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(cuda, "include"), src, "-L", lib, f"-Wl,-rpath,{lib}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", BINDING + ".tmp"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force, verbose)
     if not force and not _stale():
         return LIB
     cmd = [nvcc_path(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC,

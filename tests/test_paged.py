@@ -422,6 +422,80 @@ def test_a_captured_step(lib):
     assert eager["lengths"].tolist() == [n + 20 for n in start]
 
 
+class LongWay:
+    """TORCH_CALLS that recognises nothing."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
+def test_both_ways_into_the_library(lib, monkeypatch):
+    """the calls through TORCH_CALLS and the long way give the same bits"""
+    lengths, Hkv, G, D, P, K = [300, 40, 77], 2, 3, 64, 16, 4
+    q, k, v, kd, vd, table = setup(3, lengths, Hkv, G, 1, D, P)
+    bounds = rows(8, k.shape[0], Hkv, 2, D).sort(2).values.to(DEV)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    x = rows(9, 4, 2 * Hkv, D).to(DEV)
+    wide = torch.full((3, table.shape[1] + 3), -1, dtype=torch.int32, device=DEV)
+    wide[:, 1:-2] = dev(table)
+
+    def everything():
+        kc, vc, bd = kd.clone(), vd.clone(), bounds.clone()
+        tb = wide[:, 1:-2]
+        o = torch.empty(3, 1, Hkv * G, D, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
+        lse, pages = torch.empty(3, Hkv * G, 1, device=DEV), dev(np.zeros((3, Hkv, K)))
+        out = [dev([0] * 3), dev([0, 0], torch.int64), dev([0] * 4), dev([0] * 5, torch.int64),
+               dev([0] * 5), dev([7])]
+        lib.attn_paged_plan(dev([1, 2, -1]), dev([30, 7, 40]), wide.clone()[:, 1:-2],
+                            dev(range(9)), dev([0, 5], torch.int64), P, 5, *out)
+        lib.attn_cache_append(x[:, :Hkv], x[:, Hkv:], kc, vc, dev([5, 6, 32, -1], torch.int64), bd)
+        lib.attn_decode_paged(q.to(DEV), kc, vc, tb, dev(lengths), 0.2, o, lse, ws)
+        got = [*out, kc, vc, bd, o.clone(), lse.clone()]
+        lib.attn_page_select(q.to(DEV), bd, tb, dev(lengths), P, K, 1, 1, pages, ws)
+        lib.attn_decode_sparse(q.to(DEV), kc, vc, tb, dev(lengths), pages, None, o, lse, ws)
+        return got + [pages, o, lse]
+
+    a = everything()
+    monkeypatch.setattr(lib, "TORCH_CALLS", LongWay())
+    for x1, x2 in zip(a, everything()):
+        assert torch.equal(x1.nan_to_num(3.0), x2.nan_to_num(3.0))
+
+
+def test_refusals_before_anything_runs(lib):
+    """wrong types, shapes, devices and sizes, through both ways"""
+    lengths = [30, 20]
+    q, _, _, kd, vd, table = setup(3, lengths, 2, 2, 1, 64, 16)
+    qd, tb, ln = q.to(DEV), dev(table), dev(lengths)
+    o, lse = torch.full_like(qd, 5.0), torch.full((2, 4, 1), 5.0, device=DEV)
+    ws = torch.empty(lib.attn_decode_paged_workspace_bytes(2, 4, 2, 1, 64), dtype=torch.uint8,
+                     device=DEV)
+    good = dict(q=qd, k_cache=kd, v_cache=vd, block_table=tb, lengths=ln, o=o, lse=lse,
+                workspace=ws)
+    for name, bad in [("q", qd.float()), ("q", qd.cpu()), ("q", qd[0]), ("k_cache", kd.float()),
+                      ("v_cache", vd[:-1]), ("k_cache", kd[..., :32]), ("block_table", tb.long()),
+                      ("block_table", tb[:1]), ("block_table", tb.t()), ("lengths", ln.long()),
+                      ("lengths", ln[:1]), ("lengths", ln.cpu()), ("o", o.float()),
+                      ("o", o[:, :2]), ("lse", lse[:1]), ("workspace", ws.cpu()),
+                      ("workspace", ws[::2])]:
+        with pytest.raises(ValueError):
+            lib.attn_decode_paged(**{**good, name: bad})
+    for name, bad in [("workspace", ws[:-1]), ("workspace", ws[8:]), ("scale", 0.0),
+                      ("scale", float("nan"))]:
+        with pytest.raises(lib.CattnError):
+            lib.attn_decode_paged(**{**good, name: bad})
+    with pytest.raises(lib.CattnError):      # nine new positions
+        lib.attn_decode_paged(qd[:, :, :1].expand(2, 4, 9, 64).contiguous(), kd, vd, tb, ln)
+    with pytest.raises(lib.CattnError):      # three heads on two
+        lib.attn_decode_paged(qd[:, :3].contiguous(), kd, vd, tb, ln)
+    with pytest.raises(lib.CattnError):      # rows of the table that overlap
+        lib.attn_decode_paged(**{**good, "block_table": tb[:1].expand(2, tb.shape[1])})
+    with pytest.raises(lib.CattnError):      # a cache whose rows overlap
+        lib.attn_cache_append(qd[:1, :2, 0], qd[:1, :2, 0], kd.as_strided(kd.shape, (8, 8, 8, 1)),
+                              vd, dev([0], torch.int64))
+    torch.cuda.synchronize()
+    assert (o == 5).all() and (lse == 5).all()
+
+
 def test_on_another_stream(lib):
     """inputs written, the call made and its results read on a side stream
     that is not the current one"""
