@@ -145,8 +145,8 @@ struct PagedPlace {
   int b, ht, c, n, len;
 };
 
-// A key: where its rows of K and V begin (elements from head 0 of the pool; -1:
-// it is not held), and its position.
+// A key: where its rows of K and V begin (bytes from head 0 of the pool; -1: it
+// is not held), and its position.
 struct PagedKey {
   long long k, v;
   int pos;
@@ -218,6 +218,13 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
 // One warp's work on chunks: its ring of shared memory slots and the running
 // state of the item it is in.  UP: rows 8 .. 15 of the tile are used.  MULTI:
 // several new positions (Tq > 1), so that rows may see different keys.
+//
+// A warp waits for memory most of the time, but it has few companions (8 to 12
+// on an SM, for the rings' sake), so the length of its instruction stream
+// counts: the swizzled addresses of a slot differ from one per-lane offset by an
+// exclusive or with constants, and the running maximum only moves when a score
+// exceeds it by more than 2^8 (weights then stay below 2^8, and neither the
+// quad's exchange of maxima nor the rescaling of o is on the usual path).
 template <int D, bool UP, bool MULTI, int STAGES>
 struct PagedWarp {
   static constexpr int CK = paged_chunk(D);  // keys per chunk
@@ -228,12 +235,16 @@ struct PagedWarp {
   static constexpr int TILE = CK * D * 2;    // bytes of K (of V) per chunk
   static constexpr int CB = 2 * TILE;
   static constexpr int NR = UP ? 2 : 1;      // fragment rows of a lane: g, g + 8
+  static constexpr int RU = 32 / PC;         // rows that a 16-byte copy per lane covers
   static_assert(TILE / 16 % 32 == 0 && CK % 16 == 0 && CK <= 32 && 32 % PC == 0, "chunk");
+  static_assert(TILE % 256 == 0, "offsets inside 256 bytes may be changed by exclusive or");
 
   const PagedParams& p;
   int lane, g, t4;             // lane, fragment row, column pair
   bool same;                   // K and V have one layout
   uint8_t* ring;
+  uint32_t ring_at;            // its shared-memory address
+  uint32_t at_copy, at_k, at_v;  // the lane's offsets in a tile: copies, ldmatrix of K, of V
   int* slot_pos;               // positions of the slots' keys
   uint32_t qa[KS][4];          // query rows as mma A fragments
   float o[NO][4];              // running state of rows g (and g + 8)
@@ -245,7 +256,12 @@ struct PagedWarp {
       : p(params), lane(lane_), g(lane_ >> 2), t4(lane_ & 3),
         same(params.k_sp == params.v_sp && params.k_st == params.v_st) {
     ring = smem + warp * (STAGES * CB);
+    ring_at = pg_smem_addr(ring);
     slot_pos = reinterpret_cast<int*>(smem + paged_ring_bytes(D, STAGES)) + warp * STAGES * 32;
+    const int l7 = lane & 7, mi = lane >> 3;
+    at_copy = dec_swz<D>(lane / PC, lane % PC);
+    at_k = dec_swz<D>(l7, PC >= 4 ? mi : mi & 1);
+    at_v = dec_swz<D>((mi & 1) * 8 + l7, mi >> 1);
     clear();
   }
 
@@ -276,37 +292,47 @@ struct PagedWarp {
     }
     if (lp >= 0 && lp < p.width && lp * p.P + row < x.len) {
       const int page = p.table[x.b * p.table_sb + lp];
-      if (page >= 0 && page < p.n_pages)
-        key = PagedKey{page * p.k_sp + row * p.k_st, page * p.v_sp + row * p.v_st, lp * p.P + row};
+      if (page >= 0 && page < p.n_pages) {
+        key.k = (page * p.k_sp + row * p.k_st) * 2;
+        key.v = same ? key.k : (page * p.v_sp + row * p.v_st) * 2;
+        key.pos = lp * p.P + row;
+      }
     }
     return key;
   }
 
   // A chunk of item (b, ht) into ring slot `slot`; rows of keys that are not
   // held are zero-filled (and masked in chunk()).  A lane copies the same
-  // 16 bytes of every (32 / PC)-th row.
+  // 16 bytes of every RU-th row.
   __device__ __forceinline__ void issue(int ht, const PagedKey& key, int slot) {
-    uint8_t* sk = ring + slot * CB;
-    uint8_t* sv = sk + TILE;
+    const uint32_t to = ring_at + slot * CB + at_copy;
     const int h = ht / p.n_tiles;
-    const __nv_bfloat16* kb = p.k + h * p.k_sh + (lane % PC) * 8;
-    const __nv_bfloat16* vb = p.v + h * p.v_sh + (lane % PC) * 8;
+    const char* kb = reinterpret_cast<const char*>(p.k + h * p.k_sh) + lane % PC * 16;
+    const char* vb = reinterpret_cast<const char*>(p.v + h * p.v_sh) + lane % PC * 16;
     slot_pos[slot * 32 + lane] = key.pos;
+    const bool full = dec_ballot(lane < CK && key.k < 0) == 0u;
 #pragma unroll
     for (int u = 0; u < TILE / 16 / 32; ++u) {
-      const int row = lane / PC + 32 / PC * u, at = dec_swz<D>(row, lane % PC);
+      // row lane / PC + RU u: 512 u bytes on, its swizzle changed by constants
+      constexpr int RPL = PC >= 8 ? 1 : 8 / PC, MASK = (PC >= 8 ? 8 : PC) - 1;
+      const uint32_t at = (to ^ ((RU * u / RPL & MASK) * 16)) + 512 * u;
+      const int row = lane / PC + RU * u;
       const long long ko = dec_shfl(key.k, row), vo = same ? ko : dec_shfl(key.v, row);
-      const bool ok = ko >= 0;
-      dec_cp_async16(sk + at, kb + (ok ? ko : 0), ok);
-      dec_cp_async16(sv + at, vb + (ok ? vo : 0), ok);
+      if (full) {
+        pg_cp_async16(at, kb + ko);
+        pg_cp_async16(at + TILE, vb + vo);
+      } else {
+        pg_cp_async16(at, kb + (ko < 0 ? 0 : ko), ko >= 0);
+        pg_cp_async16(at + TILE, vb + (ko < 0 ? 0 : vo), ko >= 0);
+      }
     }
   }
 
   // Query row `gr` of cache head h: its head and new position.
   __device__ __forceinline__ long long row_head(int h, int gr, int* t) const {
-    const int gh = gr / p.Tq;
+    const int gh = MULTI ? gr / p.Tq : gr;
     *t = gr - gh * p.Tq;
-    return static_cast<long long>(h) * (p.rows / p.Tq) + gh;
+    return static_cast<long long>(h) * (p.H / p.Hkv) + gh;
   }
 
   // A new item: its query rows (zero past the last) and an empty state.
@@ -332,33 +358,36 @@ struct PagedWarp {
   // The chunk in ring slot `slot` of a request of length len.
   __device__ __forceinline__ void chunk(int slot, int len) {
     const float sl2 = p.scale_log2;
-    const uint8_t* sk = ring + slot * CB;
-    uint8_t* sv = ring + slot * CB + TILE;
+    const uint32_t sk = ring_at + slot * CB + at_k, sv = ring_at + slot * CB + TILE + at_v;
     const int* pos = slot_pos + slot * 32;
     const int pos0 = len - p.Tq;  // position of query t = 0
+    const int my_pos = lane < CK ? pos[lane] : -1;
 
-    // s = q k^T: lane's c0, c1 are row g, keys 8 nt + 2 t4, + 1; c2, c3 row g + 8
+    // s = q k^T: lane's c0, c1 are row g, keys 8 nt + 2 t4, + 1; c2, c3 row g + 8.
+    // Two sums of every other k-step each, so that the products' chain is short.
     float sc[NS][4];
 #pragma unroll
     for (int nt = 0; nt < NS; ++nt) {
+      float s2[4] = {0.f, 0.f, 0.f, 0.f};
       sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
       if constexpr (PC >= 4) {
 #pragma unroll
         for (int x = 0; x < PC / 4; ++x) {
           uint32_t r[4];
-          dec_ldsm_x4(r, sk + dec_swz<D>(nt * 8 + (lane & 7), 4 * x + (lane >> 3)));
+          pg_ldsm_x4(r, (sk ^ (64 * x)) + nt * (8 * PC * 16));
           dec_mma(sc[nt], qa[2 * x][0], qa[2 * x][1], qa[2 * x][2], qa[2 * x][3], r[0], r[1]);
-          dec_mma(sc[nt], qa[2 * x + 1][0], qa[2 * x + 1][1], qa[2 * x + 1][2], qa[2 * x + 1][3],
+          dec_mma(s2, qa[2 * x + 1][0], qa[2 * x + 1][1], qa[2 * x + 1][2], qa[2 * x + 1][3],
                   r[2], r[3]);
         }
+#pragma unroll
+        for (int c = 0; c < 2 * NR; ++c) sc[nt][c] += s2[c];
       } else {  // D = 16: one k-step
         uint32_t r[2];
-        dec_ldsm_x2(r, sk + dec_swz<D>(nt * 8 + (lane & 7), (lane >> 3) & 1));
+        pg_ldsm_x2(r, sk + nt * (8 * PC * 16));
         dec_mma(sc[nt], qa[0][0], qa[0][1], qa[0][2], qa[0][3], r[0], r[1]);
       }
     }
     // keys that are not held, and keys behind a row's position
-    const int my_pos = lane < CK ? pos[lane] : -1;
     const bool masked = dec_ballot(MULTI ? my_pos > pos0 : my_pos == kPagedNone) != 0u;
     if (masked) {
 #pragma unroll
@@ -373,34 +402,27 @@ struct PagedWarp {
     }
 
     // online softmax of the rows over this chunk
-    float alpha[NR];
-    uint32_t hi[NS][NR], lo[NS][NR];  // the weights as bf16 pairs, hi + lo
+    float mx[NR];
+    bool moves = false;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      float mx = -INFINITY;
+      mx[r] = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NS; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][2 * r], sc[nt][2 * r + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float m_new = fmaxf(m_run[r], mx * sl2);
-      const float mu = m_new == -INFINITY ? 0.f : m_new;  // no visible key yet
-      alpha[r] = dec_exp2(m_run[r] - mu);                  // 0 while m_run is -inf
-      m_run[r] = m_new;
-      float ls = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < NS; ++nt) {
-        const float p0 = dec_exp2(fmaf(sc[nt][2 * r], sl2, -mu));
-        const float p1 = dec_exp2(fmaf(sc[nt][2 * r + 1], sl2, -mu));
-        ls += p0 + p1;
-        sc[nt][2 * r] = p0;
-        sc[nt][2 * r + 1] = p1;
-        hi[nt][r] = dec_pack_bf16(p0, p1);
-        lo[nt][r] = dec_pack_bf16(p0 - dec_bf16_lo(hi[nt][r]), p1 - dec_bf16_hi(hi[nt][r]));
-      }
-      l_run[r] = fmaf(l_run[r], alpha[r], ls);
+      for (int nt = 0; nt < NS; ++nt)
+        mx[r] = fmaxf(mx[r], fmaxf(sc[nt][2 * r], sc[nt][2 * r + 1]));
+      moves = moves || mx[r] * sl2 > m_run[r] + 8.f;
     }
-    // (where no row's maximum moved, there is nothing to rescale)
-    if (dec_ballot(alpha[0] != 1.f || (UP && alpha[NR - 1] != 1.f)) != 0u) {
+    if (dec_ballot(moves) != 0u) {
+      float alpha[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        const float m_new = fmaxf(m_run[r], mx[r] * sl2);
+        alpha[r] = dec_exp2(m_run[r] - (m_new == -INFINITY ? 0.f : m_new));  // 0 from -inf
+        m_run[r] = m_new;
+        l_run[r] *= alpha[r];
+      }
 #pragma unroll
       for (int j = 0; j < NO; ++j) {
         o[j][0] *= alpha[0];
@@ -409,10 +431,28 @@ struct PagedWarp {
         o[j][3] *= alpha[NR - 1];
       }
     }
+    uint32_t hi[NS][NR], lo[NS][NR];  // the weights as bf16 pairs, hi + lo
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float mu = m_run[r] == -INFINITY ? 0.f : m_run[r];  // no visible key yet
+#pragma unroll
+      for (int nt = 0; nt < NS; ++nt) {
+        const float p0 = dec_exp2(fmaf(sc[nt][2 * r], sl2, -mu));
+        const float p1 = dec_exp2(fmaf(sc[nt][2 * r + 1], sl2, -mu));
+        l_run[r] += p0 + p1;
+        if (MULTI) {
+          sc[nt][2 * r] = p0;
+          sc[nt][2 * r + 1] = p1;
+        }
+        hi[nt][r] = dec_pack_bf16(p0, p1);
+        lo[nt][r] = dec_pack_bf16(p0 - dec_bf16_lo(hi[nt][r]), p1 - dec_bf16_hi(hi[nt][r]));
+      }
+    }
     // A key that some rows see and others do not: its value must not touch
     // those others, not even as 0 * NaN.  Its products are done one by one,
     // and its row of V is cleared for the matrix product below.
     if (MULTI && masked) {
+      uint8_t* v = ring + slot * CB + TILE;
       for (int key = 0; key < CK; ++key) {
         const int kp = pos[key];
         if (kp <= pos0 || kp == kPagedNone) continue;
@@ -428,8 +468,7 @@ struct PagedWarp {
         }
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-          const uint32_t vv =
-              *reinterpret_cast<const uint32_t*>(sv + dec_swz<D>(key, j) + 4 * t4);
+          const uint32_t vv = *reinterpret_cast<const uint32_t*>(v + dec_swz<D>(key, j) + 4 * t4);
 #pragma unroll
           for (int r = 0; r < NR; ++r)
             if (kp <= row_pos[r]) {
@@ -438,7 +477,7 @@ struct PagedWarp {
             }
         }
         __syncwarp();  // every lane has read the row
-        if (lane < PC) *reinterpret_cast<uint4*>(sv + dec_swz<D>(key, lane)) = uint4{0, 0, 0, 0};
+        if (lane < PC) *reinterpret_cast<uint4*>(v + dec_swz<D>(key, lane)) = uint4{0, 0, 0, 0};
       }
       __syncwarp();  // the cleared rows are visible
     }
@@ -449,9 +488,8 @@ struct PagedWarp {
     for (int kk = 0; kk < CK / 16; ++kk) {
 #pragma unroll
       for (int jj = 0; jj < D / 16; ++jj) {
-        const int mi = lane >> 3;
         uint32_t r[4];
-        dec_ldsm_x4_t(r, sv + dec_swz<D>(kk * 16 + (mi & 1) * 8 + (lane & 7), 2 * jj + (mi >> 1)));
+        pg_ldsm_x4_t(r, (sv ^ (32 * jj)) + kk * (16 * PC * 16));
         const uint32_t b1 = UP ? hi[2 * kk][NR - 1] : lo[2 * kk][0];
         const uint32_t b3 = UP ? hi[2 * kk + 1][NR - 1] : lo[2 * kk + 1][0];
         dec_mma(o[2 * jj], hi[2 * kk][0], b1, hi[2 * kk + 1][0], b3, r[0], r[1]);
@@ -612,7 +650,7 @@ __global__ void __launch_bounds__(kPagedThreads, UP && D == 128 ? 2 : 3)
     paged_item_kernel(const PagedParams p, int ctas) {
   dec_grid_dep_wait();
   dec_grid_dep_launch();
-  uint8_t* smem = dec_dynamic_smem();
+  uint8_t* smem = pg_dynamic_smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int HT = p.Hkv * p.n_tiles, item = static_cast<int>(blockIdx.x) / ctas;
   const int rank = static_cast<int>(blockIdx.x) - item * ctas;
@@ -693,7 +731,7 @@ template <int D, bool UP, bool MULTI>
 __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const PagedParams p) {
   dec_grid_dep_wait();
   dec_grid_dep_launch();
-  uint8_t* smem = dec_dynamic_smem();
+  uint8_t* smem = pg_dynamic_smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D, kPagedStages)) + kPagedWarps * kPagedStages * 32;
   int* totals = pre + kPagedThreads;

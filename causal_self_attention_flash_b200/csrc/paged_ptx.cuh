@@ -11,6 +11,41 @@ namespace cattn {
 
 constexpr unsigned kFullWarp = 0xffffffffu;
 
+// The kernel's dynamic shared memory, 1024-byte aligned, and shared-memory
+// addresses as 32-bit numbers (alignment of the number = that of the place).
+__device__ __forceinline__ uint8_t* pg_dynamic_smem() {
+  extern __shared__ __align__(1024) uint8_t pg_smem_base[];
+  return pg_smem_base;
+}
+__device__ __forceinline__ uint32_t pg_smem_addr(const void* p) { return dec_smem_addr(p); }
+// dec_cp_async16, dec_ldsm_x4, _x4_t and _x2 with such an address.
+__device__ __forceinline__ void pg_cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void pg_cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void pg_ldsm_x4(uint32_t (&r)[4], uint32_t row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(row)
+               : "memory");
+}
+__device__ __forceinline__ void pg_ldsm_x4_t(uint32_t (&r)[4], uint32_t row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(row)
+               : "memory");
+}
+__device__ __forceinline__ void pg_ldsm_x2(uint32_t (&r)[2], uint32_t row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];\n"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(row)
+               : "memory");
+}
+
 // The value of lane `src` (0..31) of the warp.
 __device__ __forceinline__ int dec_shfl(int v, int src) { return __shfl_sync(kFullWarp, v, src); }
 __device__ __forceinline__ float dec_shfl(float v, int src) {

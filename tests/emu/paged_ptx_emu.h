@@ -1,6 +1,6 @@
 // Host definitions of the paged-cache kernels' warp primitives (the functions
-// of paged_ptx.cuh), for the CPU emulator: indexed shuffles, ballots, the
-// cluster rank, warp sums, bit casts.
+// of paged_ptx.cuh), for the CPU emulator: shared-memory addresses, indexed
+// shuffles, ballots, the cluster rank, warp sums, bit casts.
 #pragma once
 
 #include <atomic>
@@ -20,6 +20,27 @@ struct alignas(16) longlong2 {
 namespace cattn {
 
 constexpr unsigned kFullWarp = 0xffffffffu;
+
+// Shared-memory addresses: offsets into the CTA's dynamic shared memory.
+inline uint8_t* pg_dynamic_smem() { return emu::t_cta->dsmem; }
+inline uint32_t pg_smem_addr(const void* p) {
+  return static_cast<uint32_t>(static_cast<const uint8_t*>(p) - emu::t_cta->dsmem);
+}
+inline void pg_cp_async16(uint32_t dst, const void* src) {
+  dec_cp_async16(emu::t_cta->dsmem + dst, src, true);
+}
+inline void pg_cp_async16(uint32_t dst, const void* src, bool valid) {
+  dec_cp_async16(emu::t_cta->dsmem + dst, src, valid);
+}
+inline void pg_ldsm_x4(uint32_t (&r)[4], uint32_t row) {
+  dec_ldsm_x4(r, emu::t_cta->dsmem + row);
+}
+inline void pg_ldsm_x4_t(uint32_t (&r)[4], uint32_t row) {
+  dec_ldsm_x4_t(r, emu::t_cta->dsmem + row);
+}
+inline void pg_ldsm_x2(uint32_t (&r)[2], uint32_t row) {
+  dec_ldsm_x2(r, emu::t_cta->dsmem + row);
+}
 
 namespace emu_detail {
 template <typename T>
