@@ -52,7 +52,7 @@ constexpr int kPagedMaxWarps = kPagedMaxCtas * kPagedWarps;
 constexpr int kPagedMinRun = 2;                   // chunks that a warp takes at least
 constexpr int kPagedRows = 16;                    // query rows per item
 constexpr int kPagedNone = 0x7fffffff;            // position of a key that is not held
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 512;
 
 // Keys per chunk: 4 KB of K and 4 KB of V at D >= 64; at most 32, one lane
 // per key.
@@ -905,13 +905,14 @@ __host__ __device__ constexpr int paged_item_ctas(long long items, long long chu
 //   o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
 // Grid: (CTAs of paged_decode_kernel) * n_y; CTA (c, y) takes rows y, y + n_y,
 // ... of the items that begin in CTA c's warps.  A team of warps takes a row
-// of an item, 32 parts at a time: the lanes read the parts' (m, l) at once,
-// then the warp adds up the o of those that hold keys.
+// of an item: all its parts at once where they are few, else 32 at a time: the
+// lanes read the parts' (m, l), then the warp adds up the o of those that hold
+// keys.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedParams p, int n_y) {
   constexpr int NW = kMergeThreads / 32;
   constexpr int VEC = D >= 128 ? 4 : D >= 64 ? 2 : 1;  // columns of a lane
-  constexpr int ILP = 4;                               // parts in flight
+  constexpr int ILP = 8;                               // parts in flight
   dec_grid_dep_wait();
   dec_grid_dep_launch();
   float* sh = reinterpret_cast<float*>(dec_dynamic_smem());  // [NW][2 + D]
@@ -946,18 +947,42 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
     float M = -INFINITY, L = 0.f, acc[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
-    if (in) {
+    auto place = [&](int i) { return (2LL * (gw + i) + (i == 0)) * p.R + row; };
+    if (in && c.n_parts <= ILP * team) {
+      // few parts: all of them at once
+      float2 ml[ILP];
+      float x[ILP][VEC];
+#pragma unroll
+      for (int u = 0; u < ILP; ++u) {
+        const int i = k + u * team;
+        const bool there = i < c.n_parts;
+        ml[u] = there ? p.part_ml[place(i)] : float2{-INFINITY, 0.f};
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          x[u][v] = there && mine ? p.part_o[place(i) * D + lane * VEC + v] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < ILP; ++u) M = fmaxf(M, ml[u].x);
+      const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int u = 0; u < ILP; ++u) {
+        const bool empty = ml[u].y == 0.f;  // (nothing was written to its o)
+        const float f = empty ? 0.f : ml[u].x == -INFINITY ? 1.f : dec_exp2(ml[u].x - mu);
+        L = fmaf(f, ml[u].y, L);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) acc[v] = fmaf(f, empty ? 0.f : x[u][v], acc[v]);
+      }
+    } else if (in) {
       for (int i0 = 32 * k; i0 < c.n_parts; i0 += 32 * team) {
         const int i = i0 + lane;
-        const long long at = (2LL * (gw + i) + (i == 0)) * p.R + row;
-        const float2 ml = i < c.n_parts ? p.part_ml[at] : float2{-INFINITY, 0.f};
+        const float2 ml = i < c.n_parts ? p.part_ml[place(i)] : float2{-INFINITY, 0.f};
         unsigned live = dec_ballot(ml.y != 0.f);  // (a NaN is live)
         float m = ml.x;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         const float m_new = fmaxf(M, m), mu = m_new == -INFINITY ? 0.f : m_new;
-        const float fa = exp2f(M - mu);
-        const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - mu);
+        const float fa = dec_exp2(M - mu);
+        const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : dec_exp2(ml.x - mu);
         float l = f * ml.y;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -972,10 +997,9 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
             const int src = live != 0u ? dec_lowest(live) : -1;
             live &= live - 1u;
             w[u] = dec_shfl(f, src < 0 ? 0 : src);
-            const long long a = (2LL * (gw + i0 + src) + (i0 + src == 0)) * p.R + row;
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
-              x[u][v] = src >= 0 && mine ? p.part_o[a * D + lane * VEC + v] : 0.f;
+              x[u][v] = src >= 0 && mine ? p.part_o[place(i0 + src) * D + lane * VEC + v] : 0.f;
             if (src < 0) w[u] = 0.f;
           }
 #pragma unroll
@@ -984,6 +1008,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
             for (int v = 0; v < VEC; ++v) acc[v] = fmaf(w[u], x[u][v], acc[v]);
         }
       }
+    }
+    if (in) {
       if (k > 0) {
         float* to = sh + warp * (2 + D);
         if (lane == 0) {
