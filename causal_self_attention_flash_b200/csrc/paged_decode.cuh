@@ -67,11 +67,24 @@ __host__ __device__ constexpr int paged_smem_bytes(int D, int stages) {
   return paged_ring_bytes(D, stages) + kPagedWarps * stages * 32 * 4 + (kPagedThreads + 8) * 4;
 }
 
-// Where a cut item begins: its partial results are slot 1 of warp w and
-// slot 0 of the n_parts - 1 warps behind it (n_parts = 0: none begins in w).
+// Where a cut item begins (n_parts = 0: none does in this warp), and where its
+// parts are: slot 1 of this warp; slot 0 of the n_same warps behind it in its
+// CTA; of the first warp of the n_mid CTAs behind that, whose shares lie in the
+// item as a whole; and of the first warps of one more CTA.
 struct PagedCut {
-  int b, ht, n_parts, pad;
+  int b, ht, n_parts, where;  // where = 4 n_mid + n_same
+
+  // The slot of part i of an item that begins in warp gw.
+  __host__ __device__ long long slot(int gw, int i) const {
+    const int n_same = where & 3, n_mid = where >> 2, cta = gw / kPagedWarps;
+    if (i == 0) return 2LL * gw + 1;
+    if (i <= n_same) return 2LL * (gw + i);
+    i -= n_same;
+    if (i <= n_mid) return 2LL * kPagedWarps * (cta + i);
+    return 2LL * (kPagedWarps * (cta + n_mid + 1) + i - n_mid - 1);
+  }
 };
+static_assert(kPagedWarps == 4, "PagedCut packs a warp's place in two bits");
 
 // Workspace: PagedCut[kPagedMaxWarps], then (m, l) and o of two slots per
 // warp with R = min(16, G Tq) rows each.
@@ -780,13 +793,17 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     left = static_cast<int>(S + static_cast<long long>(warp + 1) * share / kPagedWarps - s);
     if (left > 0) use = paged_locate<D>(p, HT, nb, pre, s, lane);
   }
-  // the warp that holds flat chunk x (at or behind S), and so the parts of an
-  // item that begins in this warp and ends with chunk x
-  auto parts_to = [&](long long x) {
+  // the cut of an item that begins in this warp and ends with flat chunk x
+  auto cut_to = [&](const PagedPlace& item, long long x) {
     if (x >= W) x = W - 1;
     const long long c = ((x + 1) * nc - 1) / W, cs = c * W / nc, ce = (c + 1) * W / nc;
-    const long long w = ((x - cs + 1) * kPagedWarps - 1) / (ce - cs);
-    return static_cast<int>(c * kPagedWarps + w - gw) + 1;
+    // the last warp that holds some of it; only the first if all of c's share is the item's
+    const int w = static_cast<int>(((x - cs + 1) * kPagedWarps - 1) / (ce - cs));
+    const int last = c > cta && x == ce - 1 ? 0 : w;
+    const int n_same = together ? 0 : c > cta ? kPagedWarps - 1 - warp : w - warp;
+    const int n_mid = c > cta ? static_cast<int>(c) - cta - 1 : 0;
+    return PagedCut{item.b, item.ht, 1 + n_same + n_mid + (c > cta ? last + 1 : 0),
+                    4 * n_mid + n_same};
   };
 
   PagedWarp<D, UP, MULTI, kPagedStages> k(p, smem, warp, lane);
@@ -848,10 +865,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
         k.store(p.part_ml + part, p.part_o + part * D, p.R, D);
       }
       if (begins && !ends)  // cut here: the warps that hold its other chunks
-        cut = PagedCut{use.b, use.ht,
-                       parts_to(S + static_cast<long long>(warp + 1) * share / kPagedWarps - 1 +
-                                (use.n - 1 - use.c)),
-                       0};
+        cut = cut_to(use, S + static_cast<long long>(warp + 1) * share / kPagedWarps - 1 +
+                              (use.n - 1 - use.c));
       begins = true;
       fresh = true;
     }
@@ -880,10 +895,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
       }
     }
     if (warp == 0 && first.c == 0 && !whole)
-      cut = PagedCut{first.b, first.ht, parts_to(S + first.n - 1), 0};
+      cut = cut_to(first, S + first.n - 1);
   }
-  // nothing in slot 0 of a warp whose chunks are in the CTA's part, or that has none
-  if (together ? warp > 0 : E == S || s == S + static_cast<long long>(warp + 1) * share / kPagedWarps)
+  // nothing in slot 0 of a warp without chunks
+  if (!together && s == S + static_cast<long long>(warp + 1) * share / kPagedWarps)
     if (lane < p.R) p.part_ml[2LL * gw * p.R + lane] = float2{-INFINITY, 0.f};
   if (lane == 0) p.cuts[gw] = cut;
 }
@@ -905,139 +920,103 @@ __host__ __device__ constexpr int paged_item_ctas(long long items, long long chu
 //   o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
 // Grid: (CTAs of paged_decode_kernel) * n_y; CTA (c, y) takes rows y, y + n_y,
 // ... of the items that begin in CTA c's warps.  A team of warps takes a row
-// of an item: all its parts at once where they are few, else 32 at a time: the
-// lanes read the parts' (m, l), then the warp adds up the o of those that hold
-// keys.
+// of an item, each four parts at a time.  Latency is all that counts here, and
+// part of it is the fetch of the code itself: the kernel is kept small, and
+// its registers few, so that it is resident before the last CTA ends.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedParams p, int n_y) {
+__global__ void __launch_bounds__(kMergeThreads, 2) paged_merge_kernel(const PagedParams p, int n_y) {
   constexpr int NW = kMergeThreads / 32;
   constexpr int VEC = D >= 128 ? 4 : D >= 64 ? 2 : 1;  // columns of a lane
-  constexpr int ILP = 8;                               // parts in flight
+  constexpr int ILP = 4;                               // parts in flight
   dec_grid_dep_wait();
   dec_grid_dep_launch();
   float* sh = reinterpret_cast<float*>(dec_dynamic_smem());  // [NW][2 + D]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = static_cast<int>(blockIdx.x) / n_y, y = static_cast<int>(blockIdx.x) - cta * n_y;
-  PagedCut cut[kPagedWarps];
-  int n_cuts = 0;
-#pragma unroll
-  for (int w = 0; w < kPagedWarps; ++w) {
-    cut[w] = p.cuts[cta * kPagedWarps + w];
-    n_cuts += cut[w].n_parts > 0;
-  }
-  if (n_cuts == 0) return;
+  // lanes 0 .. 3 read the cuts of the CTA's warps
+  PagedCut mine = lane < kPagedWarps ? p.cuts[cta * kPagedWarps + lane] : PagedCut{0, 0, 0, 0};
+  const unsigned begun = dec_ballot(mine.n_parts > 0);
+  if (begun == 0u) return;
   const int per_y = (p.R - y + n_y - 1) / n_y;  // rows of an item for this CTA
-  const int units = n_cuts * per_y;
+  const int units = dec_popc(begun) * per_y;
   int team = NW;                                // warps per (item, row)
   while (team > 1 && team * units > NW) team /= 2;
-  const int per = NW / team, k = warp % team;
-  const bool mine = lane * VEC < D;
-  for (int base = 0; base < units; base += per) {
-    const int unit = base + warp / team;
-    int n = unit / per_y, row = y + (unit - n * per_y) * n_y, gw = -1;
-    PagedCut c{0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kPagedWarps; ++w)
-      if (cut[w].n_parts > 0 && n-- == 0) {
-        c = cut[w];
-        gw = cta * kPagedWarps + w;
-      }
-    const int h = c.ht / p.n_tiles, r0 = (c.ht - h * p.n_tiles) * kPagedRows;
-    const bool in = unit < units && gw >= 0 && r0 + row < p.rows;
+  const int k = warp & (team - 1);
+  const bool has = lane * VEC < D;
+#pragma unroll 1
+  for (int base = 0; base < units; base += NW / team) {
+    const int unit = base + warp / team, nth = unit / per_y, row = y + (unit - nth * per_y) * n_y;
+    unsigned left = begun;
+    for (int i = 0; i < nth; ++i) left &= left - 1u;
+    const int w = left != 0u ? dec_lowest(left) : 0, gw = cta * kPagedWarps + w;
+    PagedCut c;
+    c.b = dec_shfl(mine.b, w);
+    c.ht = dec_shfl(mine.ht, w);
+    c.n_parts = dec_shfl(mine.n_parts, w);
+    c.where = dec_shfl(mine.where, w);
+    const int h = c.ht / p.n_tiles, gr = (c.ht - h * p.n_tiles) * kPagedRows + row;
+    const bool in = unit < units && gr < p.rows;
     float M = -INFINITY, L = 0.f, acc[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
-    auto place = [&](int i) { return (2LL * (gw + i) + (i == 0)) * p.R + row; };
-    if (in && c.n_parts <= ILP * team) {
-      // few parts: all of them at once
+#pragma unroll 1
+    for (int i = k; in && i < c.n_parts; i += ILP * team) {
       float2 ml[ILP];
       float x[ILP][VEC];
 #pragma unroll
       for (int u = 0; u < ILP; ++u) {
-        const int i = k + u * team;
-        const bool there = i < c.n_parts;
-        ml[u] = there ? p.part_ml[place(i)] : float2{-INFINITY, 0.f};
+        const bool there = i + u * team < c.n_parts;
+        const long long at = c.slot(gw, there ? i + u * team : 0) * p.R + row;
+        ml[u] = p.part_ml[at];
+        if (!there) ml[u] = float2{-INFINITY, 0.f};
 #pragma unroll
-        for (int v = 0; v < VEC; ++v)
-          x[u][v] = there && mine ? p.part_o[place(i) * D + lane * VEC + v] : 0.f;
+        for (int v = 0; v < VEC; ++v) x[u][v] = has ? p.part_o[at * D + lane * VEC + v] : 0.f;
       }
+      float m = M;
 #pragma unroll
-      for (int u = 0; u < ILP; ++u) M = fmaxf(M, ml[u].x);
-      const float mu = M == -INFINITY ? 0.f : M;
+      for (int u = 0; u < ILP; ++u) m = fmaxf(m, ml[u].x);
+      const float mu = m == -INFINITY ? 0.f : m, fa = dec_exp2(M - mu);
+      M = m;
+      L *= fa;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[v] *= fa;
 #pragma unroll
       for (int u = 0; u < ILP; ++u) {
-        const bool empty = ml[u].y == 0.f;  // (nothing was written to its o)
+        const bool empty = ml[u].y == 0.f;  // (its o may not have been written; a NaN goes on)
         const float f = empty ? 0.f : ml[u].x == -INFINITY ? 1.f : dec_exp2(ml[u].x - mu);
         L = fmaf(f, ml[u].y, L);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) acc[v] = fmaf(f, empty ? 0.f : x[u][v], acc[v]);
       }
-    } else if (in) {
-      for (int i0 = 32 * k; i0 < c.n_parts; i0 += 32 * team) {
-        const int i = i0 + lane;
-        const float2 ml = i < c.n_parts ? p.part_ml[place(i)] : float2{-INFINITY, 0.f};
-        unsigned live = dec_ballot(ml.y != 0.f);  // (a NaN is live)
-        float m = ml.x;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float m_new = fmaxf(M, m), mu = m_new == -INFINITY ? 0.f : m_new;
-        const float fa = dec_exp2(M - mu);
-        const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : dec_exp2(ml.x - mu);
-        float l = f * ml.y;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-        M = m_new;
-        L = fmaf(L, fa, l);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) acc[v] *= fa;
-        while (live != 0u) {
-          float x[ILP][VEC], w[ILP];
-#pragma unroll
-          for (int u = 0; u < ILP; ++u) {
-            const int src = live != 0u ? dec_lowest(live) : -1;
-            live &= live - 1u;
-            w[u] = dec_shfl(f, src < 0 ? 0 : src);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-              x[u][v] = src >= 0 && mine ? p.part_o[place(i0 + src) * D + lane * VEC + v] : 0.f;
-            if (src < 0) w[u] = 0.f;
-          }
-#pragma unroll
-          for (int u = 0; u < ILP; ++u)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) acc[v] = fmaf(w[u], x[u][v], acc[v]);
-        }
-      }
     }
-    if (in) {
-      if (k > 0) {
+    if (team > 1) {
+      if (in && k > 0) {
         float* to = sh + warp * (2 + D);
-        if (lane == 0) {
-          to[0] = M;
-          to[1] = L;
-        }
+        to[0] = M;
+        to[1] = L;
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          if (mine) to[2 + lane * VEC + v] = acc[v];
+          if (has) to[2 + lane * VEC + v] = acc[v];
       }
-    }
-    if (team > 1) __syncthreads();
-    if (in && k == 0) {
-      for (int j = 1; j < team; ++j) {
+      __syncthreads();
+#pragma unroll 1
+      for (int j = 1; in && k == 0 && j < team; ++j) {
         const float* from = sh + (warp + j) * (2 + D);
         float fa, fb;
         paged_join(from[0], from[1], M, L, fa, fb);
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          acc[v] = fmaf(acc[v], fa, mine ? fb * from[2 + lane * VEC + v] : 0.f);
+          acc[v] = fmaf(acc[v], fa, has ? fb * from[2 + lane * VEC + v] : 0.f);
       }
-      const int gr = r0 + row, gh = gr / p.Tq, t = gr - gh * p.Tq;
-      const long long hq = static_cast<long long>(h) * (p.rows / p.Tq) + gh;
+    }
+    if (in && k == 0) {
+      const int gh = gr / p.Tq, t = gr - gh * p.Tq;
+      const long long hq = static_cast<long long>(h) * (p.H / p.Hkv) + gh;
       __nv_bfloat16* ob = p.o + c.b * p.o_sb + hq * p.o_sh + t * p.o_st;
       const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
       for (int v = 0; v < VEC; ++v)
-        if (mine) ob[lane * VEC + v] = __float2bfloat16_rn(acc[v] * inv);
+        if (has) ob[lane * VEC + v] = __float2bfloat16_rn(acc[v] * inv);
       if (lane == 0)
         p.lse[(c.b * static_cast<long long>(p.H) + hq) * p.Tq + t] = paged_lse(M, L);
     }
