@@ -905,15 +905,19 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
 
 // CTAs per item of paged_item_kernel, or 0 for paged_decode_kernel, from the
 // items and the chunks that the table (the list) has room for; the lengths are
-// not known here.  As many CTAs as are resident at once; then the item kernel
-// where no warp has more than 9 chunks (16 x 12 heads x 1,024 keys of 64: 14.4
-// against 21.6 us for the other kernel; 4 x 8 x 2,048 of 128: 13.5, 18.3), the
-// other one for longer items, whose lengths may differ more (32 x 8 x 100 to
-// 1,000 keys of 128: 28.1, 23.6; 2 x 16 x 8,192: 35.3, 34.4).
+// not known here.  As many CTAs as are resident at once (128 items of 2,048
+// listed keys of 128: 37.9, 31.6 and 42.8 us with 2, 3 and 4); then the item
+// kernel where no warp has more than 12 chunks (those: 38.6 us for the other
+// kernel; 16 x 12 heads x 1,024 keys of 64: 14.1, 20.8; 4 x 8 x 2,048 of 128:
+// 12.6, 17.2), the other one for longer items, whose lengths may differ more
+// (32 x 8 x 100 to 1,000 keys of 128: 24.4, 22.4; 2 x 16 x 8,192: 33.1, 32.2).
 __host__ __device__ constexpr int paged_item_ctas(long long items, long long chunks) {
-  int ctas = 1;
-  while (ctas < 8 && 2 * ctas * items <= kItemSlots && chunks > kPagedWarps * ctas) ctas *= 2;
-  return items * ctas <= 2 * kItemSlots && chunks <= 9LL * kPagedWarps * ctas ? ctas : 0;
+  long long ctas = kItemSlots / items, most = (chunks + kPagedWarps - 1) / kPagedWarps;
+  if (ctas > 8) ctas = 8;
+  if (ctas > most) ctas = most;
+  if (ctas < 1) ctas = 1;
+  return items * ctas <= 2 * kItemSlots && chunks <= 12 * kPagedWarps * ctas
+             ? static_cast<int>(ctas) : 0;
 }
 
 // Joins the parts of the cut items:  M = max m_i,
