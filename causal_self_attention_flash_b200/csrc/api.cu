@@ -876,12 +876,12 @@ template <int D>
 cattn_status append_impl(const AppendParams& p, cudaStream_t s) {
   const int tile = append_tile(p.n);
   const long long blocks = p.bounds
-                               ? (p.n + tile - 1) / tile
+                               ? 2 * ((p.n + tile - 1) / tile)
                                : (p.n * p.Hkv * (D / 8) + kAppendThreads - 1) / kAppendThreads;
   if (blocks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
   clear_stale_error();
   LaunchTimer t(K_CACHE, s);
-  const dim3 g(static_cast<unsigned>(blocks)), b(kAppendThreads);
+  const dim3 g(static_cast<unsigned>(blocks)), b(p.bounds ? kBoundsThreads : kAppendThreads);
   const cudaError_t e =
       p.bounds ? launch_dependent(true, cache_append_bounds_kernel<D>, g, b, append_smem_bytes(),
                                   s, p, tile)
@@ -1074,7 +1074,8 @@ cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, const void* 
                                void* stream) {
   cattn_status st = check_paged(1, Hkv, Hkv, D, n_pages, page_size, 1);
   if (st != CATTN_OK) return st;
-  if (n < 0 || n > (1LL << 40)) return CATTN_ERR_INVALID_ARG;
+  if (n < 0 || n > (1LL << 40) || static_cast<long long>(n_pages) * page_size > (1LL << 32))
+    return CATTN_ERR_INVALID_ARG;
   if (n == 0) return CATTN_OK;
   if (!k_new || !v_new || !slots || !k_cache || !v_cache) return CATTN_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8) || !aligned(k_cache, 16) ||
@@ -1103,6 +1104,7 @@ cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, const void* 
   p.Hkv = Hkv;
   p.P = page_size;
   p.n_rows = static_cast<long long>(n_pages) * page_size;
+  p.mul = append_mul(page_size);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (D) {
     case 16: return append_impl<16>(p, s);

@@ -304,9 +304,9 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PlanPa
 // slots[i] % P); a slot outside the cache is skipped.  With bounds, the lowest
 // and highest value of each channel of a page's keys are kept beside it:
 //   lo_d = min over the page's keys of k_d,  hi_d = max
-// A run of new rows with ascending slots in one page is done by the threads
-// of its first row, so nothing is updated twice; a run that starts at the
-// page's first row starts its bounds over.  (NaN in, NaN out.)
+// A run of neighbouring rows of one page is done by one thread per 8 channels,
+// row after row, so nothing is updated twice; the page's first row starts its
+// bounds over.  (NaN in, NaN out.)
 //
 // The bound is memory: each row is read and written once.
 
@@ -321,10 +321,19 @@ struct AppendParams {
   __nv_bfloat16* bounds;    // (n_pages, Hkv, 2, D) or null
   long long n;
   int Hkv, P;
-  long long n_rows;         // n_pages P
+  long long n_rows;         // n_pages P, at most 2^32
+  // slot / P as the high word of (2 slot) mul, mul = floor(2^63 / P) + 1: that
+  // exceeds slot / P by at most slot / 2^63 < 1 / P (P <= 2^30), too little to
+  // reach the next whole number.  (A 64-bit division takes as long as a load.)
+  unsigned long long mul;
+  __device__ __forceinline__ long long page(long long slot) const {
+    return static_cast<long long>(dec_mulhi(2 * static_cast<unsigned long long>(slot), mul));
+  }
 };
+inline unsigned long long append_mul(int P) { return (1ull << 63) / static_cast<unsigned>(P) + 1; }
 
 constexpr int kAppendThreads = 256;
+constexpr int kBoundsThreads = 128;   // of the form with bounds
 constexpr int kAppendILP = 8;         // rows of a run in flight per thread
 constexpr int kAppendMaxTile = 32;    // tokens per CTA, a lane each
 
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
   if (i >= p.n) return;
   const long long slot = p.slots[i];
   if (slot < 0 || slot >= p.n_rows) return;
-  const long long page = slot / p.P, off = slot - page * p.P;
+  const long long page = p.page(slot), off = slot - page * p.P;
   const uint4 k =
       *reinterpret_cast<const uint4*>(p.kn + i * p.kn_st + h * p.kn_sh + pc * 8);
   const uint4 v =
@@ -355,11 +364,11 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
   *reinterpret_cast<uint4*>(p.v + page * p.v_sp + h * p.v_sh + off * p.v_st + pc * 8) = v;
 }
 
-// With bounds.  Grid: ceil(n / tile) CTAs; a CTA takes the runs that begin
-// among its `tile` tokens, to their ends.  Unit: 8 channels of K or of V of
-// one head of a run; its thread reads kAppendILP rows at a time.
+// With bounds.  Grid: two CTAs, one for K and one for V, per `tile` tokens; a
+// CTA takes the runs that begin among these, to their ends.  Unit: 8 channels
+// of one head of a run; its thread reads kAppendILP rows at a time.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kBoundsThreads)
     cache_append_bounds_kernel(const AppendParams p, int tile) {
   constexpr int PC = D / 8;
   dec_grid_dep_wait();
@@ -368,19 +377,23 @@ __global__ void __launch_bounds__(kAppendThreads)
   int* run_at = reinterpret_cast<int*>(run_slot + kAppendMaxTile);     // [32]
   int* run_len = run_at + kAppendMaxTile;                              // [32]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long i0 = static_cast<long long>(blockIdx.x) * tile;
+  const bool keys = (blockIdx.x & 1) == 0;
+  const long long i0 = static_cast<long long>(blockIdx.x >> 1) * tile;
   auto valid = [&](long long slot) { return slot >= 0 && slot < p.n_rows; };
-  // token j goes on with the run of token j - 1
+  // token j goes on with the run of token j - 1: it is in the same page, in the
+  // next row (1) or another one (2)
   auto goes_on = [&](long long j) {
-    if (j <= 0 || j >= p.n) return false;
-    const long long slot = p.slots[j];
-    return valid(slot) && p.slots[j - 1] == slot - 1 && slot % p.P != 0;
+    if (j <= 0 || j >= p.n) return 0;
+    const long long slot = p.slots[j], before = p.slots[j - 1];
+    if (!valid(slot) || !valid(before)) return 0;
+    return p.page(slot) != p.page(before) ? 0 : slot == before + 1 ? 1 : 2;
   };
   const bool in = lane < tile && i0 + lane < p.n;
   const long long slot = in ? p.slots[i0 + lane] : -1;
-  const bool on = in && goes_on(i0 + lane);
-  const unsigned stops = ~dec_ballot(on);                     // no run goes on there
-  const unsigned leads = dec_ballot(valid(slot) && !on);
+  const int on = in ? goes_on(i0 + lane) : 0;
+  const unsigned stops = ~dec_ballot(on != 0);                // no run goes on there
+  const unsigned jumps = dec_ballot(on == 2);                 // or not in the next row
+  const unsigned leads = dec_ballot(valid(slot) && on == 0);
   const int n_runs = dec_popc(leads);
   if (n_runs == 0) return;
   if (warp == 0) {
@@ -389,10 +402,14 @@ __global__ void __launch_bounds__(kAppendThreads)
     const unsigned behind = lane < 31 ? stops & inside & (~0u << (lane + 1)) : 0u;
     int len = behind != 0u ? dec_lowest(behind) - lane : tile - lane;
     const bool open = ((leads >> lane) & 1u) != 0u && behind == 0u;
+    const unsigned until = behind != 0u ? (1u << dec_lowest(behind)) - 1u : ~0u;
+    bool jump = lane < 31 && (jumps & inside & until & (~0u << (lane + 1))) != 0u;
     if (dec_ballot(open) != 0u) {
       long long j = i0 + tile;
       for (;; j += 32) {
-        const unsigned end = ~dec_ballot(goes_on(j + lane));
+        const int further = goes_on(j + lane);
+        const unsigned end = ~dec_ballot(further != 0), off = dec_ballot(further == 2);
+        if (open && (end == 0u ? off : off & ((end & (0u - end)) - 1u)) != 0u) jump = true;
         if (end != 0u) {
           j += dec_lowest(end);
           break;
@@ -403,34 +420,52 @@ __global__ void __launch_bounds__(kAppendThreads)
     if ((leads >> lane) & 1u) {
       const int r = dec_popc(leads & ((1u << lane) - 1u));
       run_slot[r] = slot;
-      run_at[r] = lane;
+      run_at[r] = jump ? lane | 64 : lane;   // 64: the rows are not in order
       run_len[r] = len;
     }
   }
   __syncthreads();
-  const int per_run = 2 * p.Hkv * PC;
-  for (int u = tid; u < n_runs * per_run; u += kAppendThreads) {
-    const int r = u / per_run, rest = u - r * per_run;
-    const bool keys = rest < p.Hkv * PC;
-    const int hp = keys ? rest : rest - p.Hkv * PC, h = hp / PC, pc = hp - h * PC;
-    const long long first = run_slot[r], page = first / p.P, i = i0 + run_at[r];
-    const int off = static_cast<int>(first - page * p.P), n = run_len[r];
+  const int per_run = p.Hkv * PC;
+  for (int u = tid; u < n_runs * per_run; u += kBoundsThreads) {
+    const int r = u / per_run, hp = u - r * per_run, h = hp / PC, pc = hp - h * PC;
+    const long long first = run_slot[r], page = p.page(first), i = i0 + (run_at[r] & 31);
+    const int off = static_cast<int>(first - page * p.P);
+    const bool jump = (run_at[r] & 64) != 0;
+    const int n = run_len[r];
     const long long from_st = keys ? p.kn_st : p.vn_st, to_st = keys ? p.k_st : p.v_st;
     const __nv_bfloat16* from = keys ? p.kn + i * p.kn_st + h * p.kn_sh + pc * 8
                                      : p.vn + i * p.vn_st + h * p.vn_sh + pc * 8;
-    __nv_bfloat16* to = keys ? p.k + page * p.k_sp + h * p.k_sh + off * p.k_st + pc * 8
-                             : p.v + page * p.v_sp + h * p.v_sh + off * p.v_st + pc * 8;
+    __nv_bfloat16* to = keys ? p.k + page * p.k_sp + h * p.k_sh + pc * 8
+                             : p.v + page * p.v_sp + h * p.v_sh + pc * 8;
     uint4* bl = reinterpret_cast<uint4*>(p.bounds + ((page * p.Hkv + h) * 2) * D + pc * 8);
     uint4 lo, hi;
-    if (keys) {
-      if (off != 0) {  // the page goes on
-        lo = *bl;
-        hi = bl[D / 8];
-      } else {
-        lo = hi = *reinterpret_cast<const uint4*>(from);
+    if (keys && off != 0) {  // the page goes on
+      lo = *bl;
+      hi = bl[D / 8];
+    } else if (keys) {
+      lo = hi = *reinterpret_cast<const uint4*>(from);
+    }
+    auto join = [&](const uint4& x) {
+      lo.x = dec_bf16_min(lo.x, x.x);
+      lo.y = dec_bf16_min(lo.y, x.y);
+      lo.z = dec_bf16_min(lo.z, x.z);
+      lo.w = dec_bf16_min(lo.w, x.w);
+      hi.x = dec_bf16_max(hi.x, x.x);
+      hi.y = dec_bf16_max(hi.y, x.y);
+      hi.z = dec_bf16_max(hi.z, x.z);
+      hi.w = dec_bf16_max(hi.w, x.w);
+    };
+    if (jump) {  // one after another
+      for (int t = 0; t < n; ++t) {
+        const uint4 x = *reinterpret_cast<const uint4*>(from + t * from_st);
+        const long long row = p.slots[i + t] - page * p.P;
+        *reinterpret_cast<uint4*>(to + row * to_st) = x;
+        if (keys && row == 0) lo = hi = x;
+        if (keys) join(x);
       }
     }
-    for (int t = 0; t < n; t += kAppendILP) {
+    to += off * to_st;
+    for (int t = 0; t < n && !jump; t += kAppendILP) {
       uint4 x[kAppendILP];
 #pragma unroll
       for (int j = 0; j < kAppendILP; ++j)  // (past the last: the last again)
@@ -440,16 +475,7 @@ __global__ void __launch_bounds__(kAppendThreads)
         if (t + j < n) *reinterpret_cast<uint4*>(to + (t + j) * to_st) = x[j];
       if (keys) {
 #pragma unroll
-        for (int j = 0; j < kAppendILP; ++j) {
-          lo.x = dec_bf16_min(lo.x, x[j].x);
-          lo.y = dec_bf16_min(lo.y, x[j].y);
-          lo.z = dec_bf16_min(lo.z, x[j].z);
-          lo.w = dec_bf16_min(lo.w, x[j].w);
-          hi.x = dec_bf16_max(hi.x, x[j].x);
-          hi.y = dec_bf16_max(hi.y, x[j].y);
-          hi.z = dec_bf16_max(hi.z, x[j].z);
-          hi.w = dec_bf16_max(hi.w, x[j].w);
-        }
+        for (int j = 0; j < kAppendILP; ++j) join(x[j]);
       }
     }
     if (keys) {

@@ -71,6 +71,11 @@ __device__ __forceinline__ float dec_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// High word of the 128-bit product.
+__device__ __forceinline__ unsigned long long dec_mulhi(unsigned long long a,
+                                                        unsigned long long b) {
+  return __umul64hi(a, b);
+}
 // Sum over the warp's lanes.
 __device__ __forceinline__ int dec_warp_sum(int v) { return __reduce_add_sync(kFullWarp, v); }
 __device__ __forceinline__ unsigned dec_warp_min(unsigned v) {

@@ -392,15 +392,16 @@ CATTN_API cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t*
  *                 0 .. n_pages * page_size - 1 is skipped
  *   bounds        bf16 (n_pages, Hkv, 2, D) contiguous, or NULL: the lowest
  *                 and the highest value of each channel of a page's keys,
- *                 kept for attn_page_select.  A run of tokens with ascending
- *                 slots in a page joins its bounds; if it starts at the
- *                 page's first row they start over.  NaN in, NaN out.
+ *                 kept for attn_page_select.  A token joins the bounds of its
+ *                 page; one in the page's first row starts them over.  NaN
+ *                 in, NaN out.
  *
- * Slots must differ from one another, and with bounds the tokens of a page
- * must form one run of neighbours (as in the plan); otherwise the rows (the
- * bounds) concerned are either token's.  The inputs must not overlap the
- * cache.  Errors: CATTN_ERR_INVALID_ARG (a cache layout that overlaps itself
- * included), CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  n = 0 is a no-op. */
+ * With bounds, the tokens of a page must be neighbours in the list (as in the
+ * plan); they are then written one after another.  Otherwise slots must
+ * differ.  A list that breaks this leaves either token's row (and bounds) in
+ * the page concerned.  The inputs must not overlap the cache.  Errors:
+ * CATTN_ERR_INVALID_ARG (a cache layout that overlaps itself included),
+ * CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  n = 0 is a no-op. */
 CATTN_API cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, const void* v_new,
                                          cattn_layout lvn, long long n, int Hkv, int D,
                                          int n_pages, int page_size, const int64_t* slots,

@@ -167,7 +167,7 @@ static void plan() {
 template <int D>
 static void run_append(const AppendParams& p, int tile) {
   if (p.bounds) {
-    emu::launch_ex(static_cast<unsigned>((p.n + tile - 1) / tile), kAppendThreads,
+    emu::launch_ex(static_cast<unsigned>(2 * ((p.n + tile - 1) / tile)), kBoundsThreads,
                    append_smem_bytes(), 1, cache_append_bounds_kernel<D>, p, tile);
     return;
   }
@@ -185,6 +185,7 @@ static void append() {
   const int D = a[2];
   p.P = a[4];
   p.n_rows = a[3] * a[4];
+  p.mul = append_mul(p.P);
   p.kn = in<__nv_bfloat16>(1);
   p.vn = in<__nv_bfloat16>(2);
   p.slots = in<long long>(3);

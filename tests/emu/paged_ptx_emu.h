@@ -106,6 +106,9 @@ inline float dec_exp2(float x) {
   const float y = std::exp2(x);
   return y < 0x1p-126f ? 0.f : y;
 }
+inline unsigned long long dec_mulhi(unsigned long long a, unsigned long long b) {
+  return static_cast<unsigned long long>(static_cast<unsigned __int128>(a) * b >> 64);
+}
 inline unsigned dec_cluster_rank() { return emu::t_cta->rank; }
 inline uint32_t dec_bf16_absmax(uint32_t m, uint32_t x) {
   x &= 0x7fff7fffu;

@@ -311,7 +311,10 @@ def test_append_nan_keys_and_odd_pages(emu):
     for tile in (1, 5, 32):
         run_append(emu, list(range(7, 60)), 2, 64, 3, 20, tile=tile)
     run_append(emu, list(range(3, 120)), 1, 16, 1, 130, tile=3)     # one run over many tiles
-    run_append(emu, [5, 5 + 2 ** 40, 6, 7], 1, 16, 1, 16, tile=4)   # a run that breaks off
+    run_append(emu, [5, 5 + 2 ** 40], 1, 16, 1, 16, tile=4)         # a run that breaks off
+    # rows of a page in any order, with gaps, one of them twice, its first row late
+    run_append(emu, [9, 12, 10, 10, 8, 15, 3, 1], 2, 32, 2, 8, tile=8)
+    run_append(emu, [9, 12, 10, 10, 8, 15, 3, 1], 2, 32, 2, 8, tile=3)
 
 
 # ----------------------------------------------------------------- select
