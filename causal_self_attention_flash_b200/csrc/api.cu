@@ -756,6 +756,7 @@ cattn_status check_paged(int B, int H, int Hkv, int D, int n_pages, int P, int w
   const cattn_status st = check_shape(B, H, 1, D);
   if (st != CATTN_OK) return st;
   if (Hkv < 1 || H % Hkv != 0 || n_pages < 1 || P < 1 || width < 1) return CATTN_ERR_INVALID_ARG;
+  if (H > (1 << 20)) return CATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(width) * P > (1LL << 30)) return CATTN_ERR_INVALID_ARG;
   return CATTN_OK;
 }
@@ -829,6 +830,8 @@ cattn_status paged_decode(const void* q, cattn_layout lq, const void* k, cattn_l
   p.rows = static_cast<int>(rows);
   p.n_tiles = (p.rows + kPagedRows - 1) / kPagedRows;
   p.R = p.rows < kPagedRows ? p.rows : kPagedRows;
+  if (B * chunks > (1LL << 38) / (static_cast<long long>(Hkv) * p.n_tiles))
+    return CATTN_ERR_INVALID_ARG;
   if (workspace_bytes < static_cast<size_t>(paged_workspace_bytes(p.R, D)))
     return CATTN_ERR_INVALID_ARG;
   int dev;

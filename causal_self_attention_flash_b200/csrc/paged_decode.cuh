@@ -98,9 +98,9 @@ __host__ __device__ constexpr long long paged_workspace_bytes(int R, int D) {
   return paged_o_offset(R) + 2LL * kPagedMaxWarps * R * D * 4;
 }
 
-// n / P for 0 <= n <= 2^30 as (n mul) >> shift: with shift = 31 + L, 2^L >= P,
+// n / P for 0 <= n < 2^31 as (n mul) >> shift: with shift = 31 + L, 2^L >= P,
 // and mul = floor(2^shift / P) + 1 <= 2^32, n mul / 2^shift exceeds n / P by at
-// most n / 2^shift <= 1 / (2 P), too little to reach the next whole number.
+// most n / 2^shift < 1 / P, too little to reach the next whole number.
 struct PageDivider {
   unsigned long long mul;
   int shift;
@@ -140,10 +140,13 @@ struct PagedParams {
 
 // Keys of request b that its items enumerate (sparse: of the listed pages),
 // and the chunks they take; an item without keys has one, empty, chunk.
+__device__ __forceinline__ int paged_length(const PagedParams& p, int b) {
+  const int len = p.lengths[b];
+  return len > 0 ? len : 0;
+}
 __device__ __forceinline__ int paged_keys(const PagedParams& p, int len) {
-  if (len < 0) len = 0;
   if (p.pages != nullptr)  // (a list holds at most 2^30 keys)
-    return len >= p.n_sel * p.P ? p.n_sel * p.P : (p.by_P(len + p.P - 1)) * p.P;
+    return len >= p.n_sel * p.P ? p.n_sel * p.P : p.by_P(len + p.P - 1) * p.P;
   const int cap = p.width * p.P;
   return len < cap ? len : cap;
 }
@@ -172,7 +175,7 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, int HT, PagedPl
   if (++x.ht < HT) return;
   x.ht = 0;
   if (++x.b >= p.B) return;  // behind the last item
-  x.len = p.lengths[x.b];
+  x.len = paged_length(p, x.b);
   x.n = paged_chunks<D>(p, x.len);
 }
 
@@ -206,7 +209,7 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
   for (int b0 = t * nb; b0 < (t + 1) * nb; b0 += 32) {
     const int b = b0 + lane;
     const bool in = lane < (t + 1) * nb - b0 && b < p.B;
-    const int len = in ? p.lengths[b] : 0;
+    const int len = in ? paged_length(p, b) : 0;
     const int n = in ? paged_chunks<D>(p, len) : 0;
     const int incl = warp_scan(n, lane);
     const unsigned hit = dec_ballot(run + incl > y);
@@ -298,7 +301,8 @@ struct PagedWarp {
     if (lane < CK && x.b < p.B) {
       if (p.pages != nullptr) {
         const int h = x.ht / p.n_tiles;
-        if (vk < paged_keys(p, x.len)) lp = p.pages[(static_cast<long long>(x.b) * p.Hkv + h) * p.n_sel + li];
+        if (vk < paged_keys(p, x.len))
+          lp = p.pages[(static_cast<long long>(x.b) * p.Hkv + h) * p.n_sel + li];
       } else {
         lp = li;
       }
@@ -670,7 +674,7 @@ __global__ void __launch_bounds__(kPagedThreads, UP && D == 128 ? 2 : 3)
   PagedPlace x;
   x.b = item / HT;
   x.ht = item - x.b * HT;
-  x.len = p.lengths[x.b];
+  x.len = paged_length(p, x.b);
   x.n = paged_chunks<D>(p, x.len);
   x.c = rank * kPagedWarps + warp;
   const int step = ctas * kPagedWarps, h = x.ht / p.n_tiles;
@@ -746,7 +750,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
   dec_grid_dep_launch();
   uint8_t* smem = pg_dynamic_smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D, kPagedStages)) + kPagedWarps * kPagedStages * 32;
+  int* pre = reinterpret_cast<int*>(smem + paged_ring_bytes(D, kPagedStages)) +
+             kPagedWarps * kPagedStages * 32;
   int* totals = pre + kPagedThreads;
   const int HT = p.Hkv * p.n_tiles;
 
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
   int mine = 0;
   for (int i = 0; i < nb; ++i) {
     const int b = tid * nb + i;
-    if (b < p.B) mine += paged_chunks<D>(p, p.lengths[b]);
+    if (b < p.B) mine += paged_chunks<D>(p, paged_length(p, b));
   }
   const int incl = warp_scan(mine, lane);
   if (lane == 31) totals[warp] = incl;

@@ -339,8 +339,8 @@ CATTN_API cattn_status attn_decode(const void* q, cattn_layout lq, const void* k
  *     attn_decode_paged  attention of the new positions, or
  *     attn_page_select and attn_decode_sparse, over the best pages only.
  *
- * Limits common to these calls: D as above, H a multiple of Hkv (query head
- * i reads cache head i / (H / Hkv)), width * page_size <= 2^30, page_size
+ * Limits common to these calls: D as above, H <= 2^20 a multiple of Hkv (query
+ * head i reads cache head i / (H / Hkv)), width * page_size <= 2^30, page_size
  * >= 1.  Layout rules as for the _strided calls.  Lengths below 0 count as
  * 0. */
 
@@ -426,7 +426,7 @@ CATTN_API cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, co
  * tables have room for short requests only, else two; results do not depend on
  * the run.  Errors: CATTN_ERR_INVALID_ARG (as attn_decode;
  * Hkv, page_size, width or table_stride out of range; tables with room for
- * 2^31 or more chunks of 32 keys, 16 at D = 128, in all; a small or misaligned
+ * 2^31 or more chunks of 32 keys, 16 at D = 128, or over 2^38 for all heads; a small or misaligned
  * workspace), CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  B = 0 or H = 0 is a
  * no-op. */
 CATTN_API size_t attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int Tq, int D);

@@ -43,6 +43,8 @@ def test_decode_refusals(sparse, bad):
 
 def test_decode_refuses_more_chunks_than_it_counts():
     assert decode(B=1 << 20, width=1 << 20, stride=1 << 20) == INVALID
+    assert decode(B=1 << 10, H=1 << 18, Hkv=1 << 18, width=1 << 17, stride=1 << 17) == INVALID
+    assert decode(B=1, H=1 << 21, Hkv=1) == INVALID
 
 
 @pytest.mark.parametrize("sparse", [False, True])

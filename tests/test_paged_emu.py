@@ -99,6 +99,7 @@ def run_decode(emu, lengths, Hkv, G, Tq, D, P, grid, *, layout=1, spare=0, holes
 @pytest.mark.parametrize("lengths,Hkv,G,Tq,D,P,grid", [
     ([1], 1, 1, 1, 16, 16, 1),
     ([0, 5, -3, 1], 1, 1, 1, 64, 16, 2),       # empty requests between others
+    ([-2 ** 31, 20, -2 ** 31], 1, 2, 8, 64, 16, 1),
     ([37], 1, 1, 1, 32, 16, 1),
     ([100, 3], 2, 4, 1, 64, 16, 1),            # several items per warp
     ([70], 1, 2, 1, 128, 16, 1),               # one item over several warps
