@@ -291,29 +291,27 @@ struct PagedWarp {
     for (int j = 0; j < NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   }
 
-  // The page, the row in it and the position of the lane's key of chunk x.
+  // The lane's key of chunk x.  (The list and the table are read as far as they
+  // go, whatever the length: its own load need not have arrived.)
   __device__ __forceinline__ PagedKey look_up(const PagedPlace& x) const {
-    PagedKey key{-1, -1, kPagedNone};
     const int vk = x.c * CK + lane;
     const int li = p.by_P(vk);
     const int row = vk - li * p.P;
-    int lp = -1;
+    int lp = -1, page = -1;
     if (lane < CK && x.b < p.B) {
-      if (p.pages != nullptr) {
-        const int h = x.ht / p.n_tiles;
-        if (vk < paged_keys(p, x.len))
-          lp = p.pages[(static_cast<long long>(x.b) * p.Hkv + h) * p.n_sel + li];
-      } else {
-        lp = li;
-      }
+      lp = li;
+      if (p.pages != nullptr)
+        lp = li < p.n_sel ? p.pages[(static_cast<long long>(x.b) * p.Hkv + x.ht / p.n_tiles) *
+                                        p.n_sel + li]
+                          : -1;
+      if (lp >= 0 && lp < p.width) page = p.table[x.b * p.table_sb + lp];
     }
-    if (lp >= 0 && lp < p.width && lp * p.P + row < x.len) {
-      const int page = p.table[x.b * p.table_sb + lp];
-      if (page >= 0 && page < p.n_pages) {
-        key.k = (page * p.k_sp + row * p.k_st) * 2;
-        key.v = same ? key.k : (page * p.v_sp + row * p.v_st) * 2;
-        key.pos = lp * p.P + row;
-      }
+    PagedKey key{-1, -1, kPagedNone};
+    if (page >= 0 && page < p.n_pages && lp * p.P + row < x.len &&
+        (p.pages == nullptr || vk < paged_keys(p, x.len))) {
+      key.k = (page * p.k_sp + row * p.k_st) * 2;
+      key.v = same ? key.k : (page * p.v_sp + row * p.v_st) * 2;
+      key.pos = lp * p.P + row;
     }
     return key;
   }
@@ -688,8 +686,7 @@ __global__ void __launch_bounds__(kPagedThreads, UP && D == 128 ? 2 : 3)
     return k.look_up(y);
   };
 #pragma unroll
-  for (int i = 0; i < kItemStages; ++i)
-    if (i < left) key[i] = look_up(i);
+  for (int i = 0; i < kItemStages; ++i) key[i] = look_up(i);
 #pragma unroll
   for (int i = 0; i < kItemStages; ++i) {
     if (i < left) k.issue(x.ht, key[i], i);
