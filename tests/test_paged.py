@@ -63,6 +63,9 @@ def test_decode(lib, D, P, G, Tq):
     ([3000, 5], 1, 5, 8, 64, 48),              # 40 rows: three tiles
     ([700 + 13 * i for i in range(20)], 3, 1, 1, 64, 16),
     ([(i * 53) % 90 for i in range(700)], 2, 2, 1, 32, 16),
+    ([(i * 7) % 23 for i in range(5000)], 1, 1, 1, 16, 8),   # 40 requests per thread of the scan
+    ([20000, 9001], 2, 5, 4, 64, 16),          # 20 rows: two tiles, cut over many CTAs
+    ([12000, 0, 7, 12345], 1, 2, 1, 16, 16),   # one short and one empty item among cut ones
 ])
 def test_decode_shapes(lib, lengths, Hkv, G, Tq, D, P):
     run_case(lib, 5, lengths, Hkv, G, Tq, D, P)
@@ -85,6 +88,42 @@ def test_sparse(lib, D, G, Tq):
             pages[b, h, :count] = np.sort(rng.permutation(opaged.n_pages_of(n, P))[:count])
     pages[0, 0, 3] = 1000                      # lists nothing
     run_case(lib, 8, lengths, Hkv, G, Tq, D, P, pages=pages)
+
+
+def test_sparse_long_lists(lib):
+    """more listed keys than one cluster takes: the flat kernel"""
+    rng = np.random.default_rng(1)
+    B, Hkv, P, K = 40, 4, 16, 200
+    lengths = [5000 if b % 3 else 100 + b for b in range(B)]
+    pages = np.full((B, Hkv, K), -1)
+    for b, n in enumerate(lengths):
+        count = opaged.n_pages_of(n, P)
+        for h in range(Hkv):
+            some = np.sort(rng.permutation(count)[:K])
+            pages[b, h, :len(some)] = some
+    run_case(lib, 12, lengths, Hkv, 2, 1, 64, P, pages=pages)
+
+
+def test_two_calls_at_once(lib):
+    """calls on two streams, each with its own workspace, give the bits of a
+    call alone"""
+    cases = []
+    for seed, lengths, Hkv, G, D in ((1, [30000], 2, 4, 128), (2, [900, 4000, 70], 4, 1, 64)):
+        q, _, _, kd, vd, table = setup(seed, lengths, Hkv, G, 1, D, 16)
+        args = (q.to(DEV), kd, vd, dev(table), dev(lengths))
+        want = [x.clone() for x in lib.attn_decode_paged(*args)]
+        ws = torch.empty(lib.attn_decode_paged_workspace_bytes(len(lengths), Hkv * G, Hkv, 1, D),
+                         dtype=torch.uint8, device=DEV)
+        cases.append((args, want, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        for args, want, ws, stream in cases:
+            with torch.cuda.stream(stream):
+                got.append((lib.attn_decode_paged(*args, workspace=ws), want))
+    torch.cuda.synchronize()
+    for (o, lse), (wo, wl) in got:
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
 
 
 def test_decode_matches_the_contiguous_cache(lib):
