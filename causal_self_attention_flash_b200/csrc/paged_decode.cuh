@@ -156,6 +156,11 @@ __device__ __forceinline__ int paged_chunks(const PagedParams& p, int len) {
   return n > 0 ? n : 1;
 }
 
+// What an item costs its warp beside its chunks, in chunks: its query rows,
+// lengths and table row are trips to memory that nothing hides.  On the flat
+// axis every item begins with that many empty places (c < 0).
+__host__ __device__ constexpr int paged_item_cost(int D) { return D == 128 ? 2 : 4; }
+
 // A place on the flat axis: chunk c of the n of item (b, ht).
 struct PagedPlace {
   int b, ht, c, n, len;
@@ -168,10 +173,14 @@ struct PagedKey {
   int pos;
 };
 
+// On to the next chunk; `units` are the places from x to the end of the run.
 template <int D>
-__device__ __forceinline__ void paged_next(const PagedParams& p, int HT, PagedPlace& x) {
+__device__ __forceinline__ void paged_next(const PagedParams& p, int HT, PagedPlace& x,
+                                           int& units) {
+  --units;
   if (++x.c < x.n) return;
   x.c = 0;
+  units -= paged_item_cost(D);
   if (++x.ht < HT) return;
   x.ht = 0;
   if (++x.b >= p.B) return;  // behind the last item
@@ -194,9 +203,9 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {
   return v;
 }
 
-// The place of flat chunk x: request b holds chunks HT * before(b) up to
-// HT * before(b + 1), before = the chunks of one head of the requests in
-// front.  pre[t] is before(t * nb).  (The lengths are read again here; the
+// Flat place x: request b holds the places HT * before(b) up to
+// HT * before(b + 1), before = the chunks and costs of one head of the requests
+// in front.  pre[t] is before(t * nb).  (The lengths are read again here; the
 // clamps keep every index in range should a caller change them meanwhile.)
 template <int D>
 __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT, int nb,
@@ -210,7 +219,7 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
     const int b = b0 + lane;
     const bool in = lane < (t + 1) * nb - b0 && b < p.B;
     const int len = in ? paged_length(p, b) : 0;
-    const int n = in ? paged_chunks<D>(p, len) : 0;
+    const int n = in ? paged_chunks<D>(p, len) + paged_item_cost(D) : 0;
     const int incl = warp_scan(n, lane);
     const unsigned hit = dec_ballot(run + incl > y);
     if (hit != 0u) {
@@ -222,7 +231,8 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
       const int before = run + dec_shfl(incl, src) - r.n;
       const long long rem = x - static_cast<long long>(before) * HT;
       r.ht = static_cast<int>(rem / r.n);
-      r.c = static_cast<int>(rem - static_cast<long long>(r.ht) * r.n);
+      r.c = static_cast<int>(rem - static_cast<long long>(r.ht) * r.n) - paged_item_cost(D);
+      r.n -= paged_item_cost(D);
       if (r.ht >= HT) r.ht = HT - 1;
       return r;
     }
@@ -757,7 +767,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
   int mine = 0;
   for (int i = 0; i < nb; ++i) {
     const int b = tid * nb + i;
-    if (b < p.B) mine += paged_chunks<D>(p, paged_length(p, b));
+    if (b < p.B) mine += paged_chunks<D>(p, paged_length(p, b)) + paged_item_cost(D);
   }
   const int incl = warp_scan(mine, lane);
   if (lane == 31) totals[warp] = incl;
@@ -784,18 +794,27 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
   const int share = static_cast<int>(E - S);
   PagedPlace use = paged_locate<D>(p, HT, nb, pre, S, lane);
   const bool together = use.c + share <= use.n;  // one item's
-  const PagedPlace first = use;
-  const int step = together ? kPagedWarps : 1;
-  long long s = S + warp;
-  int left = share > warp ? (share - warp + kPagedWarps - 1) / kPagedWarps : 0;
+  // its first place that is a chunk, and how many of them
+  PagedPlace first = use;
+  if (first.c < 0) first.c = 0;
+  const int chunks = use.c + share - first.c;
+  // this warp's places: `units` of them up to flat place e (together: turns)
+  long long e = E;
+  int units = share;
   if (together) {
-    use.c += warp;
+    use.c = first.c + warp;
+    units = chunks > warp ? (chunks - warp + kPagedWarps - 1) / kPagedWarps : 0;
   } else {
-    s = S + static_cast<long long>(warp) * share / kPagedWarps;
-    left = static_cast<int>(S + static_cast<long long>(warp + 1) * share / kPagedWarps - s);
-    if (left > 0) use = paged_locate<D>(p, HT, nb, pre, s, lane);
+    const long long s = S + static_cast<long long>(warp) * share / kPagedWarps;
+    e = S + static_cast<long long>(warp + 1) * share / kPagedWarps;
+    units = static_cast<int>(e - s);
+    if (units > 0) use = paged_locate<D>(p, HT, nb, pre, s, lane);
+    if (use.c < 0) {
+      units += use.c;
+      use.c = 0;
+    }
   }
-  // the cut of an item that begins in this warp and ends with flat chunk x
+  // the cut of an item that begins in this warp and ends with flat place x
   auto cut_to = [&](const PagedPlace& item, long long x) {
     if (x >= W) x = W - 1;
     const long long c = ((x + 1) * nc - 1) / W, cs = c * W / nc, ce = (c + 1) * W / nc;
@@ -809,36 +828,43 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
   };
 
   PagedWarp<D, UP, MULTI, kPagedStages> k(p, smem, warp, lane);
+  const bool none = units <= 0;
   PagedPlace get = use;
-  int to_look = left;
+  int ahead = units;  // the places from `get` on
   PagedKey key[kPagedStages], next{-1, -1, kPagedNone};
-  int hts[kPagedStages];
-  auto look_up = [&](PagedKey& to) {  // the next chunk's keys, and on to the one behind it
-    to = k.look_up(get);
-    const int ht = get.ht;
-    if (--to_look > 0) {
-      if (together) get.c += step; else paged_next<D>(p, HT, get);
+  int hts[kPagedStages], next_ht = 0;
+  auto on = [&](PagedPlace& x, int& left) {
+    if (together) {
+      x.c += kPagedWarps;
+      --left;
+    } else {
+      paged_next<D>(p, HT, x, left);
     }
-    return ht;
+  };
+  auto look_up = [&](PagedKey& to, int& ht) {  // the next chunk's keys, and on to the one behind
+    if (ahead <= 0) return false;
+    to = k.look_up(get);
+    ht = get.ht;
+    on(get, ahead);
+    return true;
   };
   // the first chunks' keys are looked up together, then one ahead; one commit
   // group per ring slot, empty when the run is shorter
+  bool there[kPagedStages];
 #pragma unroll
-  for (int i = 0; i < kPagedStages; ++i)
-    if (i < left) hts[i] = look_up(key[i]);
+  for (int i = 0; i < kPagedStages; ++i) there[i] = look_up(key[i], hts[i]);
 #pragma unroll
   for (int i = 0; i < kPagedStages; ++i) {
-    if (i < left) k.issue(hts[i], key[i], i);
+    if (there[i]) k.issue(hts[i], key[i], i);
     dec_cp_async_commit();
   }
-  int next_ht = 0, to_issue = left - kPagedStages;
-  if (to_issue > 0) next_ht = look_up(next);
+  bool more = look_up(next, next_ht);
 
   bool begins = use.c == 0;  // the current item's first chunk is this warp's
   bool fresh = true;
   PagedCut cut{0, 0, 0, 0};
   int slot = 0;
-  while (left > 0) {
+  while (units > 0) {
     if (fresh) {
       fresh = false;
       k.begin(use);
@@ -847,37 +873,34 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
     __syncwarp();  // every lane's pieces of the chunk are in shared memory
     k.chunk(slot, use.len);
     __syncwarp();  // every lane has read the slot: refill it
-    if (to_issue > 0) {
+    if (more) {
       k.issue(next_ht, next, slot);
-      if (--to_issue > 0) next_ht = look_up(next);
+      more = look_up(next, next_ht);
     }
     dec_cp_async_commit();
     slot = slot + 1 == kPagedStages ? 0 : slot + 1;
-    --left;
-    if (together) {
-      use.c += step;
-      continue;
-    }
-    const bool ends = use.c + 1 == use.n;
-    if (ends || left == 0) {
+    const PagedPlace done = use;
+    const long long at = e - units;  // its flat place
+    on(use, units);
+    if (together) continue;
+    const bool ends = done.c + 1 == done.n;
+    if (ends || units <= 0) {
       if (ends && begins) {
-        k.finish(use);
+        k.finish(done);
       } else {
         const long long part = (2LL * gw + begins) * p.R;
         k.store(p.part_ml + part, p.part_o + part * D, p.R, D);
       }
       if (begins && !ends)  // cut here: the warps that hold its other chunks
-        cut = cut_to(use, S + static_cast<long long>(warp + 1) * share / kPagedWarps - 1 +
-                              (use.n - 1 - use.c));
+        cut = cut_to(done, at + (done.n - 1 - done.c));
       begins = true;
       fresh = true;
     }
-    if (left > 0) paged_next<D>(p, HT, use);
   }
   dec_cp_async_wait<0>();
 
-  if (together) {
-    const bool whole = first.c == 0 && share == first.n;
+  if (together && chunks > 0) {
+    const bool whole = first.c == 0 && chunks == first.n;
     const PagedMerge<D> a(smem);
     __syncthreads();  // every warp is done with its ring
     k.store(a.ml + warp * kPagedRows, a.ov + warp * kPagedRows * a.PITCH, p.R, a.PITCH);
@@ -897,10 +920,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const Pa
       }
     }
     if (warp == 0 && first.c == 0 && !whole)
-      cut = cut_to(first, S + first.n - 1);
+      cut = cut_to(first, E - chunks + first.n - 1);
   }
   // nothing in slot 0 of a warp without chunks
-  if (!together && s == S + static_cast<long long>(warp + 1) * share / kPagedWarps)
+  if (!together && none)
     if (lane < p.R) p.part_ml[2LL * gw * p.R + lane] = float2{-INFINITY, 0.f};
   if (lane == 0) p.cuts[gw] = cut;
 }
