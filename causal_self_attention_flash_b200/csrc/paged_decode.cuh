@@ -158,7 +158,9 @@ __device__ __forceinline__ int paged_chunks(const PagedParams& p, int len) {
 
 // What an item costs its warp beside its chunks, in chunks: its query rows,
 // lengths and table row are trips to memory that nothing hides.  On the flat
-// axis every item begins with that many empty places (c < 0).
+// axis every item begins with that many empty places (c < 0).  (64 requests of
+// 10 to 12,453 keys x 8 heads of 128: 108 us without, 88 with 2; of 64: 70 and
+// 55 with 4; twice as many change nothing or cost 5 percent at D <= 32.)
 __host__ __device__ constexpr int paged_item_cost(int D) { return D == 128 ? 2 : 4; }
 
 // A place on the flat axis: chunk c of the n of item (b, ht).
@@ -750,7 +752,9 @@ __global__ void __launch_bounds__(kPagedThreads, UP && D == 128 ? 2 : 3)
 //
 // A CTA takes an even share of the flat axis.  If all of it lies in one item
 // the warps take turns at its chunks and join their results in shared
-// memory; otherwise each takes a quarter of the share.
+// memory; otherwise each takes a quarter of the share.  Where the table has
+// room for long requests: 726 MB of K and V (64 x 8 heads x 2,770 keys of 128)
+// in 127 us with the merge, 2.9 GB in 458 us (6.3 TB/s).
 template <int D, bool UP, bool MULTI>
 __global__ void __launch_bounds__(kPagedThreads, 2) paged_decode_kernel(const PagedParams p) {
   dec_grid_dep_wait();
