@@ -25,7 +25,7 @@
 //     q k^T and p v with mma.sync m16n8k16 (query rows as the A operand, at
 //     most 16) and keeps the running maximum and sum (online softmax);
 //   - an item that ends inside its warp's run is written out directly; a cut
-//     item leaves (m, l, o) per warp in the workspace and merge_kernel joins
+//     item leaves (m, l, o) per warp in the workspace, paged_merge_kernel joins
 //     them, in the order of the keys, so results repeat bit for bit.
 // p enters the second product as a bf16 pair (hi + lo, about 16 bits), so that
 // o carries no rounding but its own to bf16.  With at most 8 rows that costs no
