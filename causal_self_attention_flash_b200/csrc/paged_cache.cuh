@@ -717,7 +717,9 @@ __device__ __forceinline__ unsigned long long score_key(double s) {
 }
 
 // Reductions over the NT threads of a CTA; `sh` has two halves of three words
-// per warp, used in turn, so that one barrier each is enough.
+// per warp, used in turn, so that one barrier each is enough.  (A reduction
+// ends with reads of its half: whatever else writes to `sh` needs a barrier
+// before it.)
 template <int NT>
 struct PickReduce {
   static constexpr int NW = NT / 32;
@@ -800,8 +802,10 @@ __device__ __forceinline__ void pick_pages(const SelectParams& p, int b, int h, 
   float* shf = reinterpret_cast<float*>(sh + 6 * NW);                // [2][NW]
   unsigned long long* sums = reinterpret_cast<unsigned long long*>(shf + 2 * NW);  // [kPickNear]
   int* list = reinterpret_cast<int*>(sums + kPickNear);                            // [kPickNear]
+  int* n_list = list + kPickNear;                                                  // its entries
   PickReduce<NT> over{sh, 0};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) *n_list = 0;  // (barriers follow before it is used)
   const long long bh = static_cast<long long>(b) * p.Hkv + h;
   int* out = p.pages + bh * p.n_sel;
   const float* score = p.score + bh * p.width;
@@ -911,10 +915,8 @@ __device__ __forceinline__ void pick_pages(const SelectParams& p, int b, int h, 
   if (few) {
     // list them, sum them, and rank each among all: the keys of those chosen
     // become the highest, of the others the lowest
-    if (tid == 0) sh[0] = 0;
-    __syncthreads();
     each([&](int i, unsigned k) {
-      if (near(k)) list[dec_add_shared(sh, 1)] = i;  // (in any order)
+      if (near(k)) list[dec_add_shared(n_list, 1)] = i;  // (in any order)
     });
     __syncthreads();
     for (int j = warp; j < n_of[1]; j += NW) {
@@ -1051,7 +1053,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) page_select_kernel(const Se
 }
 
 __host__ __device__ constexpr int pick_smem_bytes() {
-  return kPickKeys * 4 + 8 * (kPickThreads / 32) * 4 + kPickNear * 12;
+  return kPickKeys * 4 + 8 * (kPickThreads / 32) * 4 + kPickNear * 12 + 16;
 }
 // Shared memory of the fused kernel: the rings, and then the choice's.
 __host__ __device__ constexpr int select_smem_bytes(int D) {

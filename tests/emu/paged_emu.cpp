@@ -5,6 +5,9 @@
 //
 //   paged_emu decode|plan|append|select in.bin out.bin
 //
+// With LATE_WARP=w in the environment, warp w of each CTA goes on late behind
+// every CTA barrier.
+//
 // in.bin is a row of arrays, each an int64 byte count and the bytes; the
 // first holds int64 parameters.  out.bin is the outputs, one behind the other.
 // The host set-up (grids, strides of packed arrays) follows api.cu.
@@ -267,6 +270,7 @@ int main(int argc, char** argv) {
   read_all(argv[2]);
   g_out = std::fopen(argv[3], "wb");
   if (!g_out) return 5;
+  if (const char* w = std::getenv("LATE_WARP")) emu::g_late_warp = std::atoi(w);
   const std::string op = argv[1];
   if (op == "decode") decode();
   else if (op == "plan") plan();

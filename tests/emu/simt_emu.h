@@ -13,6 +13,7 @@
 #pragma once
 
 #include <barrier>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -78,6 +79,10 @@ inline thread_local uint3_ t_thread, t_block;
 inline thread_local dim3 t_bdim, t_gdim;
 inline thread_local Cta* t_cta = nullptr;
 
+// Warp of each CTA that goes on late behind every CTA barrier (-1: none): what
+// the others do meanwhile must not reach what it has still to read.
+inline int g_late_warp = -1;
+
 }  // namespace emu
 
 #define threadIdx (emu::t_thread)
@@ -85,7 +90,11 @@ inline thread_local Cta* t_cta = nullptr;
 #define blockDim (emu::t_bdim)
 #define gridDim (emu::t_gdim)
 
-inline void __syncthreads() { emu::t_cta->cta_bar->arrive_and_wait(); }
+inline void __syncthreads() {
+  emu::t_cta->cta_bar->arrive_and_wait();
+  if (emu::g_late_warp == static_cast<int>(threadIdx.x / 32))
+    std::this_thread::sleep_for(std::chrono::milliseconds(40));
+}
 
 // warp barrier (full warps only, like the shuffles)
 inline void __syncwarp(unsigned mask = 0xffffffffu) {

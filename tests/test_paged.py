@@ -299,6 +299,27 @@ def test_select_ties_nan_and_pages_that_are_not_held(lib):
     check(q, bounds, table)
 
 
+def test_select_sure_pages_beside_ties(lib):
+    """sure pages in several warps and ties at the border, many heads at once
+    and again and again: the choice is the oracle's each time"""
+    L, P, K, D, Hkv = 1200, 4, 150, 64, 32
+    q, bounds, table = select_inputs(4, [L], Hkv, 1, 1, D, P)
+    bounds[:] = bounds[:1]
+    for h in range(Hkv):
+        q[0, h, 0] = bounds[0, h, 1]
+        for i in range(3 + h, 300, 37 + h):
+            bounds[table[0, i], h] *= 2 + h % 7
+    bounds[:, :, 0] = 0
+    want = opaged.select(as64(q), as64(bounds), table, [L], P, K, 1, 1)
+    qd, bd, tb, ln = q.to(DEV), bounds.to(DEV), dev(table), dev([L])
+    got = [lib.attn_page_select(qd, bd, tb, ln, P, K) for _ in range(50)]
+    wide = torch.full((1, 20000), -1, dtype=torch.int32, device=DEV)   # two launches
+    wide[:, :table.shape[1]] = tb
+    got += [lib.attn_page_select(qd, bd, wide, ln, P, K) for _ in range(50)]
+    for x in got:
+        assert np.array_equal(x.cpu().numpy(), want)
+
+
 # ---------------------------------------------------------- run together
 
 class Server:

@@ -376,3 +376,21 @@ def test_select_ties_nan_and_pages_that_are_not_held(emu):
                holes=[((0, 4), -1), ((0, 8), 10 ** 6)])
     # more pages that are not held than are left out
     run_select(emu, [40], 1, 1, 1, 16, 4, 8, holes=[((0, i), -1) for i in range(1, 7)])
+
+
+@pytest.mark.parametrize("groups", [0, 1])
+@pytest.mark.parametrize("gap", [2, 5, 100])
+def test_select_with_a_late_warp(emu, monkeypatch, groups, gap):
+    """sure pages and ties at the border, the ties that are just chosen in a
+    warp that is late behind every barrier: what the others write then must not
+    reach what it still reads.  The gap between the sure pages and the ties sets
+    how many rounds the search for the border takes."""
+    monkeypatch.setenv("LATE_WARP", "1")
+
+    def change(q, bounds, table):
+        bounds[:] = bounds[:1]
+        q.copy_(bounds[0, 0, 1].expand_as(q))
+        for i in (9, 20, 74):
+            bounds[table[0, i]] *= gap
+        bounds[:, :, 0] = 0
+    run_select(emu, [320], 1, 1, 1, 16, 4, 45, change=change, groups=groups)
