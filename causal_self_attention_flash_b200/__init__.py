@@ -499,10 +499,23 @@ def _array(t, dtype, shape, dev, what):
     return t.data_ptr()
 
 
-def _result(t, dtype, shape, dev, what):
+def _new(shape, dtype, dev, stream):
+    """Memory that a call on `stream` writes: allocated for that stream, so
+    that whatever else the allocator does with the block, before and
+    afterwards, is in order with the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)        # (1: the default stream by its other name)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _result(t, dtype, shape, dev, what, stream):
     """An output array, allocated if not given, and its address."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = _new(shape, dtype, dev, stream)
         return t, t.data_ptr()
     return t, _array(t, dtype, shape, dev, what)
 
@@ -516,13 +529,14 @@ def _table(t, B, dev):
     return t.data_ptr(), st[0] if B > 1 else shape[1], shape[1]
 
 
-def _scratch(ws, dev, need):
-    """A workspace and its bytes; `need`: a function of no arguments."""
+def _scratch(ws, dev, need, stream):
+    """A workspace, which the caller holds until the call is made, its
+    address and bytes; `need`: a function of no arguments."""
     if ws is None:
-        ws = torch.empty(max(need(), 1), dtype=torch.uint8, device=dev)
+        ws = _new((max(need(), 1),), torch.uint8, dev, stream)
     elif ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"workspace must be contiguous device memory on {dev}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _done(which, st):
@@ -561,12 +575,12 @@ def attn_paged_plan(new_tokens, lengths, block_table, free_ring, ring_state, pag
     p_table, stride, width = _table(block_table, B, dev)
     p_ring = _array(free_ring, _I32, (n_pages,), dev, "free_ring")
     p_state = _array(ring_state, _I64, (2,), dev, "ring_state")
-    lengths_out, p_lo = _result(lengths_out, _I32, (B,), dev, "lengths_out")
-    ring_state_out, p_so = _result(ring_state_out, _I64, (2,), dev, "ring_state_out")
-    cu_new, p_cu = _result(cu_new, _I32, (B + 1,), dev, "cu_new")
-    slots, p_slots = _result(slots, _I64, (n_slots,), dev, "slots")
-    positions, p_pos = _result(positions, _I32, (n_slots,), dev, "positions")
-    status, p_st = _result(status, _I32, (1,), dev, "status")
+    lengths_out, p_lo = _result(lengths_out, _I32, (B,), dev, "lengths_out", stream)
+    ring_state_out, p_so = _result(ring_state_out, _I64, (2,), dev, "ring_state_out", stream)
+    cu_new, p_cu = _result(cu_new, _I32, (B + 1,), dev, "cu_new", stream)
+    slots, p_slots = _result(slots, _I64, (n_slots,), dev, "slots", stream)
+    positions, p_pos = _result(positions, _I32, (n_slots,), dev, "positions", stream)
+    status, p_st = _result(status, _I32, (1,), dev, "status", stream)
     _call(CALL_PAGED_PLAN, p_new, p_len, p_table, stride, p_ring, p_state, B, width, n_pages,
           page_size, n_slots, p_lo, p_so, p_cu, p_slots, p_pos, p_st, _stream(stream))
     return lengths_out, ring_state_out, cu_new, slots, positions, status
@@ -626,11 +640,11 @@ def _decode_paged(which, q, k_cache, v_cache, block_table, lengths, pages, scale
         K = pages.shape[-1]
         listed = (_array(pages, _I32, (B, Hkv, K), dev, "pages"), K)
     if o is None:
-        o = torch.empty(shape, dtype=_BF16, device=dev)
+        o = _new(shape, _BF16, dev, stream)
     so = _strides(o, dev, "o", shape)
-    lse, p_lse = _result(lse, _F32, (B, H, Tq), dev, "lse")
-    p_ws, ws_bytes = _scratch(workspace, dev,
-                              lambda: attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D))
+    lse, p_lse = _result(lse, _F32, (B, H, Tq), dev, "lse", stream)
+    workspace, p_ws, ws_bytes = _scratch(
+        workspace, dev, lambda: attn_decode_paged_workspace_bytes(B, H, Hkv, Tq, D), stream)
     _call(which, q.data_ptr(), sq[0], sq[1], sq[2], k_cache.data_ptr(), sk[0], sk[1], sk[2],
           v_cache.data_ptr(), sv[0], sv[1], sv[2], D ** -0.5 if scale is None else scale, B, H,
           Hkv, Tq, D, n_pages, P, p_table, stride, width, p_len, *listed, o.data_ptr(), so[0],
@@ -685,9 +699,9 @@ def attn_page_select(q, bounds, block_table, lengths, page_size, n_select, n_fir
     p_bounds = _array(bounds, _BF16, (n_pages, Hkv, 2, D), dev, "bounds")
     p_table, stride, width = _table(block_table, B, dev)
     p_len = _array(lengths, _I32, (B,), dev, "lengths")
-    pages, p_pages = _result(pages, _I32, (B, Hkv, n_select), dev, "pages")
-    p_ws, ws_bytes = _scratch(workspace, dev,
-                              lambda: attn_page_select_workspace_bytes(B, Hkv, width))
+    pages, p_pages = _result(pages, _I32, (B, Hkv, n_select), dev, "pages", stream)
+    workspace, p_ws, ws_bytes = _scratch(
+        workspace, dev, lambda: attn_page_select_workspace_bytes(B, Hkv, width), stream)
     _call(CALL_PAGE_SELECT, q.data_ptr(), sq[0], sq[1], sq[2], p_bounds, B, H, Hkv, Tq, D, n_pages,
           page_size, p_table, stride, width, p_len, n_select, n_first, n_last, p_pages, p_ws,
           ws_bytes, _stream(stream))

@@ -577,3 +577,30 @@ def test_on_another_stream(lib):
     side.synchronize()
     ref = opaged.decode(as64(q), as64(k), as64(v), table, lengths, np.float32(0.125))
     check_decode(as64(o.cpu()), as64(lse.cpu()), ref, 500, 64)
+
+
+def test_on_another_stream_with_its_own_allocations(lib):
+    """nothing given but the inputs, a side stream that runs late, and the
+    current stream filling whatever it gets meanwhile"""
+    lengths = [20000, 400]
+    q, k, v, kd, vd, table = setup(9, lengths, 2, 2, 1, 64, 16)
+    bounds = rows(8, k.shape[0], 2, 2, 64).sort(2).values.to(DEV)
+    qd, tb, ln = q.to(DEV), dev(table), dev(lengths)
+    want = lib.attn_decode_paged(qd, kd, vd, tb, ln)
+    pages = lib.attn_page_select(qd, bounds, tb, ln, 16, 20)
+    listed = lib.attn_decode_sparse(qd, kd, vd, tb, ln, pages)
+    n = lib.attn_decode_paged_workspace_bytes(2, 4, 2, 1, 64)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(4_000_000)
+        got = [lib.attn_decode_paged(qd, kd, vd, tb, ln, stream=stream)]
+        got.append((lib.attn_page_select(qd, bounds, tb, ln, 16, 20, stream=stream),))
+        got.append(lib.attn_decode_sparse(qd, kd, vd, tb, ln, got[1][0], stream=stream))
+        junk = [torch.full((size,), 0x7f, dtype=torch.uint8, device=DEV)
+                for size in (n, n, 1 << 20, 2 * 4 * 64 * 2, 2 * 4 * 4, 2 * 2 * 20 * 4) * 3]
+        side.synchronize()
+        for x, y in zip((*want, pages, *listed), (t for g in got for t in g)):
+            assert torch.equal(x, y)
+        del junk

@@ -4,7 +4,10 @@ tensors.  Every refused call returns before it touches a device."""
 
 from __future__ import annotations
 
+import contextlib
+import gc
 import math
+import weakref
 
 import pytest
 import torch
@@ -231,3 +234,53 @@ def test_torch_calls_leave_foreign_tensors_to_the_long_way():
     assert cattn.TORCH_CALLS.append(1, 2) == -1
     assert cattn.TORCH_CALLS.plan(*["x"] * 13) == -1
     assert cattn.TORCH_CALLS.select(*[t] * 10) == -1
+
+
+def paged_calls(stream):
+    """every paged call with nothing given that it can allocate itself"""
+    i32, i64 = torch.int32, torch.int64
+    q, k = dev(2, 4, 1, 64), dev(9, 2, 16, 64)
+    t, n = dev(2, 5, dtype=i32), dev(2, dtype=i32)
+    yield 6, lambda: cattn.attn_paged_plan(n, n, t, dev(9, dtype=i32), dev(2, dtype=i64), 16, 3,
+                                           stream=stream)
+    yield 3, lambda: cattn.attn_decode_paged(q, k, k, t, n, stream=stream)
+    yield 3, lambda: cattn.attn_decode_sparse(q, k, k, t, n, dev(2, 2, 3, dtype=i32), stream=stream)
+    yield 2, lambda: cattn.attn_page_select(q, dev(9, 2, 2, 64), t, n, 16, 3, stream=stream)
+
+
+@pytest.mark.parametrize("stream", ["none", "object", "handle"])
+def test_allocations_live_until_the_call_and_belong_to_its_stream(fake, monkeypatch, stream):
+    """what a paged call allocates (outputs, workspace) is held when the library
+    is called, and was allocated under the stream that the call is made on"""
+    new, current, seen = [], [None], []
+
+    class Stream:                               # stands in for torch.cuda.Stream
+        def __init__(self, handle=99, device=None):
+            self.cuda_stream = handle
+
+    @contextlib.contextmanager
+    def under(s):
+        current.append(s.cuda_stream)
+        yield
+        current.pop()
+
+    def empty(shape, dtype, device):
+        t = dev(*shape, dtype=dtype)
+        new.append((weakref.ref(t), current[-1]))
+        return t
+
+    def call(*args):
+        gc.collect()
+        seen.append([(ref() is not None, s) for ref, s in new])
+        return 0
+    monkeypatch.setattr(cattn, "_stream", lambda s: getattr(s, "cuda_stream", s) or 0)
+    monkeypatch.setattr(cattn.torch, "empty", empty)
+    monkeypatch.setattr(cattn.torch.cuda, "stream", under)
+    monkeypatch.setattr(cattn.torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(cattn.torch.cuda, "ExternalStream", Stream)
+    fake.attn_paged_call = call
+    given, on = {"none": (None, None), "object": (Stream(55), 55), "handle": (66, 66)}[stream]
+    for count, make in paged_calls(given):
+        new.clear()
+        make()
+        assert seen[-1] == [(True, on)] * count
