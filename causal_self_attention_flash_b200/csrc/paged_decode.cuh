@@ -27,10 +27,13 @@
 //   - an item that ends inside its warp's run is written out directly; a cut
 //     item leaves (m, l, o) per warp in the workspace, paged_merge_kernel joins
 //     them, in the order of the keys, so results repeat bit for bit.
-// p enters the second product as a bf16 pair (hi + lo, about 16 bits), so that
-// o carries no rounding but its own to bf16.  With at most 8 rows that costs no
-// instruction: hi takes the fragment's rows 0 .. 7, lo its rows 8 .. 15, and
-// the two halves of the accumulator are added at the end.
+// p enters the second product as a bf16 pair, hi + lo: a relative error of at
+// most 2^-16, little beside the 2^-9 of o's own rounding to bf16.  With at most 8
+// rows the pair costs no instruction: hi takes the fragment's rows 0 .. 7, lo its
+// rows 8 .. 15, and the two halves of the accumulator are added at the end.  hi
+// is p cut off, and lo the rest of p with its last bit set: neither is zero or
+// negative where p > 0 (from 2^-110 on, where lo leaves bf16's range), so an
+// infinite value of V gives infinity in both products and not 0 inf or inf - inf.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -458,7 +461,7 @@ struct PagedWarp {
         o[j][3] *= alpha[NR - 1];
       }
     }
-    uint32_t hi[NS][NR], lo[NS][NR];  // the weights as bf16 pairs, hi + lo
+    uint32_t hi[NS][NR], lo[NS][NR];  // the weights as bf16 pairs, hi + lo (see the top)
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const float mu = m_run[r] == -INFINITY ? 0.f : m_run[r];  // no visible key yet
@@ -471,8 +474,11 @@ struct PagedWarp {
           sc[nt][2 * r] = p0;
           sc[nt][2 * r + 1] = p1;
         }
-        hi[nt][r] = dec_pack_bf16(p0, p1);
-        lo[nt][r] = dec_pack_bf16(p0 - dec_bf16_lo(hi[nt][r]), p1 - dec_bf16_hi(hi[nt][r]));
+        const unsigned u0 = dec_float_bits(p0), u1 = dec_float_bits(p1);
+        hi[nt][r] = u0 >> 16 | (u1 & 0xffff0000u);
+        lo[nt][r] =
+            dec_pack_bf16(dec_bits_float(u0 | 1u) - dec_bits_float(u0 & 0xffff0000u),
+                          dec_bits_float(u1 | 1u) - dec_bits_float(u1 & 0xffff0000u));
       }
     }
     // A key that some rows see and others do not: its value must not touch

@@ -77,6 +77,30 @@ def test_decode_pages_that_are_not_held(lib):
     run_case(lib, 6, [200, 90, 20], 2, 4, 5, 128, 16, holes=holes)
 
 
+@pytest.mark.parametrize("L", [3, 700, 20000])
+@pytest.mark.parametrize("D,G,Tq", [(16, 1, 1), (32, 9, 1), (64, 3, 2), (128, 4, 1), (128, 5, 4)])
+def test_decode_infinite_values(lib, L, D, G, Tq):
+    """an infinite value that a row sees is its result (NaN where both signs
+    meet), whatever the key's weight; other channels are as without it"""
+    lengths, P = [L, 40], 16
+    q, k, v, kd, vd, table = setup(11, lengths, 2, G, Tq, D, P)
+    scale = np.float32(D ** -0.5)
+    ref = opaged.decode(as64(q), as64(k), as64(v), table, lengths, scale)
+    seen = max(1, L - Tq + 1)                      # keys that every row with a key sees
+    for d, sign in ((0, 1), (1, -1), (2, 1), (3, -1)):
+        pos = d * (seen - 1) // 3
+        vd[table[0, pos // P], :, pos % P, d] = sign * float("inf")
+    for pos, sign in ((0, 1), (seen - 1, -1)):
+        vd[table[0, pos // P], :, pos % P, 7] = sign * float("inf")
+    o, lse = lib.attn_decode_paged(q.to(DEV), kd, vd, dev(table), dev(lengths), scale=scale)
+    o, lse = as64(o.cpu()), as64(lse.cpu())
+    some = o[0][np.isfinite(lse[0])]                # rows with a key
+    assert (some[:, [0, 2]] == np.inf).all() and (some[:, [1, 3]] == -np.inf).all()
+    assert np.isnan(some[:, 7]).all() or seen == 1
+    o[0][..., [0, 1, 2, 3, 7]] = ref[0][0][..., [0, 1, 2, 3, 7]]
+    check_decode(o, lse, ref, L, D)
+
+
 @pytest.mark.parametrize("D,G,Tq", [(64, 1, 1), (128, 4, 1), (128, 2, 3)])
 def test_sparse(lib, D, G, Tq):
     rng = np.random.default_rng(D)

@@ -176,6 +176,46 @@ def test_decode_unseen_keys_do_not_touch_a_row(emu):
     assert np.isnan(o2[:, 2:]).all() and np.isnan(lse2[:, 2:]).all()
 
 
+def decode_raw(emu, q, k, v, table, length, grid, scale):
+    """one request, packed (n_pages, Hkv, P, D) pools"""
+    (B, H, Tq, D), (n_pages, Hkv, P, _) = q.shape, k.shape
+    raw = emu("decode", [B, H, Hkv, Tq, D, n_pages, P, table.shape[1], 0, grid, 0], bits(q),
+              bits(k), bits(v), table, np.array([length], np.int32), np.zeros(0, np.int32),
+              np.array([scale], np.float32))
+    n = B * H * Tq
+    o = from_bits(raw[:2 * n * D]).astype(np.float64).reshape(B, H, Tq, D)
+    return o, np.frombuffer(raw[2 * n * D:], np.float32).astype(np.float64).reshape(B, H, Tq)
+
+
+@pytest.mark.parametrize("D,G,Tq", [(64, 2, 1), (64, 3, 2), (128, 9, 1), (16, 5, 4)])
+def test_decode_infinite_values(emu, D, G, Tq):
+    """an infinite value that a row sees is its result (NaN where both signs
+    meet), whatever the key's weight; other channels are as without it"""
+    L, P = 75, 16
+    table = np.arange(5, dtype=np.int32)[None, ::-1].copy()
+    k, v, q = rows(1, 5, 1, P, D), rows(2, 5, 1, P, D), rows(3, 1, G, Tq, D, std=1.5)
+    scale = np.float32(D ** -0.5)
+    ref = opaged.decode(as64(q), as64(k), as64(v), table, [L], scale)
+
+    def at(pos):
+        return table[0, pos // P], 0, pos % P
+    for pos, d in ((0, 0), (17, 1), (34, 2), (50, 3), (L - Tq, 4)):
+        v[at(pos)][d] = float("inf")
+        v[at(pos)][d + 5] = float("-inf")
+    v[at(3)][11], v[at(40)][11] = float("inf"), float("-inf")
+    for grid in (1, 2, -1, -2):
+        o, lse = decode_raw(emu, q, k, v, table, L, grid, scale)
+        assert (o[..., :5] == np.inf).all() and (o[..., 5:10] == -np.inf).all()
+        assert np.isnan(o[..., 11]).all()
+        o[..., [*range(10), 11]] = ref[0][..., [*range(10), 11]]
+        check_decode(o, lse, ref, L, D)
+    # one key: its weight is one
+    v[at(0)][:] = float("inf")
+    for grid in (1, -1):
+        assert (decode_raw(emu, q, k, v, table, Tq, grid, scale)[0][:, :, -1] == np.inf).all()
+        assert (decode_raw(emu, q[:, :, -1:], k, v, table, 1, grid, scale)[0] == np.inf).all()
+
+
 @pytest.mark.parametrize("Tq,G", [(1, 1), (2, 3)])
 def test_sparse(emu, Tq, G):
     pages = np.full((3, 2, 4), -1)
