@@ -56,6 +56,7 @@ constexpr int kPagedMinRun = 2;                   // chunks that a warp takes at
 constexpr int kPagedRows = 16;                    // query rows per item
 constexpr int kPagedNone = 0x7fffffff;            // position of a key that is not held
 constexpr int kMergeThreads = 512;
+constexpr float kPagedLag = 8.f;                  // how far scores rise before m_run follows, log2
 
 // Keys per chunk: 4 KB of K and 4 KB of V at D >= 64; at most 32, one lane
 // per key.
@@ -193,9 +194,12 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, int HT, PagedPl
   x.n = paged_chunks<D>(p, x.len);
 }
 
-// Natural log-sum-exp from a base-2 maximum and sum.
+// Natural log-sum-exp from a base-2 reference and the sum relative to it, which
+// lies 2 kPagedLag below the largest score at the most: brought there, so that the
+// two parts do not cancel.
 __device__ __forceinline__ float paged_lse(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  constexpr float up = 1 << static_cast<int>(2 * kPagedLag);
+  return l == 0.f ? -INFINITY : (m - 2.f * kPagedLag + log2f(l * up)) * 0.69314718055994531f;
 }
 
 // Inclusive sum over the warp's lanes.
@@ -253,9 +257,12 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedParams& p, int HT,
 // A warp waits for memory most of the time, but it has few companions (8 to 12
 // on an SM, for the rings' sake), so the length of its instruction stream
 // counts: the swizzled addresses of a slot differ from one per-lane offset by an
-// exclusive or with constants, and the running maximum only moves when a score
-// exceeds it by more than 2^8 (weights then stay below 2^8, and neither the
-// quad's exchange of maxima nor the rescaling of o is on the usual path).
+// exclusive or with constants, and the running reference m_run, which the
+// weights 2^(s - m_run) are relative to, is set 2^16 above the largest score and
+// only moves when a score comes within 2^8 of it.  (Weights stay below 2^-8, so
+// the sums over values near the largest bf16 have room for 2^8 such weights, and
+// neither the quad's exchange of maxima nor the rescaling of o is on the usual
+// path.)
 template <int D, bool UP, bool MULTI, int STAGES>
 struct PagedWarp {
   static constexpr int CK = paged_chunk(D);  // keys per chunk
@@ -431,7 +438,7 @@ struct PagedWarp {
         }
     }
 
-    // online softmax of the rows over this chunk
+    // online softmax of the rows over this chunk (m_run: see the class)
     float mx[NR];
     bool moves = false;
 #pragma unroll
@@ -440,7 +447,7 @@ struct PagedWarp {
 #pragma unroll
       for (int nt = 0; nt < NS; ++nt)
         mx[r] = fmaxf(mx[r], fmaxf(sc[nt][2 * r], sc[nt][2 * r + 1]));
-      moves = moves || mx[r] * sl2 > m_run[r] + 8.f;
+      moves = moves || mx[r] * sl2 > m_run[r] - kPagedLag;
     }
     if (dec_ballot(moves) != 0u) {
       float alpha[NR];
@@ -448,7 +455,7 @@ struct PagedWarp {
       for (int r = 0; r < NR; ++r) {
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        const float m_new = fmaxf(m_run[r], mx[r] * sl2);
+        const float m_new = fmaxf(m_run[r], fmaf(mx[r], sl2, 2.f * kPagedLag));
         alpha[r] = dec_exp2(m_run[r] - (m_new == -INFINITY ? 0.f : m_new));  // 0 from -inf
         m_run[r] = m_new;
         l_run[r] *= alpha[r];

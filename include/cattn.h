@@ -423,9 +423,10 @@ CATTN_API cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, co
  *
  * Keys past a request's length are not read.  A key that a row does not see
  * does not touch its result, whatever its values.  An infinite value that a row
- * sees is its result as in the formula, down to weights of 2^-90 of the row's
+ * sees is its result as in the formula, down to weights of 2^-80 of the row's
  * largest (below that NaN).  Weights enter the product with V as pairs of bf16
- * values, to 2^-16; sums and lse are fp32.  One launch where the
+ * values, to 2^-16; sums and lse are fp32, and no sum of finite values overflows
+ * before 2^8 keys of a row's largest weight and the largest value meet.  One launch where the
  * tables have room for short requests only, else two; results do not depend on
  * the run.  Errors: CATTN_ERR_INVALID_ARG (as attn_decode;
  * Hkv, page_size, width or table_stride out of range; tables with room for

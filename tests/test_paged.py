@@ -101,6 +101,26 @@ def test_decode_infinite_values(lib, L, D, G, Tq):
     check_decode(o, lse, ref, L, D)
 
 
+@pytest.mark.parametrize("L", [150, 9000])
+@pytest.mark.parametrize("D,G,Tq", [(16, 1, 1), (64, 3, 2), (128, 9, 1)])
+def test_decode_large_values(lib, L, D, G, Tq):
+    """scores that rise by less than the running maximum follows, with values
+    near the largest bf16: finite where the formula is"""
+    q, k, v, kd, vd, table = setup(13, [L], 1, G, Tq, D, 16)
+    q[..., 0], q[..., 1:] = 1, 0
+    kd[..., 0] = 0
+    k[..., 0] = 0
+    for i, x in enumerate((5.25, 5.5, 5.375)):      # e^5.5 < 2^8
+        pos = L - Tq - 2 + i
+        for kk, vv in ((k, v), (kd, vd)):
+            kk[table[0, pos // 16], 0, pos % 16, 0] = x
+            vv[table[0, pos // 16], 0, pos % 16, :] = 3e38 * (-1) ** i
+            vv[table[0, pos // 16], 0, pos % 16, 1::2] = 1.5e38
+    ref = opaged.decode(as64(q), as64(k), as64(v), table, [L], 1.0)
+    o, lse = lib.attn_decode_paged(q.to(DEV), kd, vd, dev(table), dev([L]), scale=1.0)
+    check_decode(as64(o.cpu()), as64(lse.cpu()), ref, L, D)
+
+
 @pytest.mark.parametrize("D,G,Tq", [(64, 1, 1), (128, 4, 1), (128, 2, 3)])
 def test_sparse(lib, D, G, Tq):
     rng = np.random.default_rng(D)

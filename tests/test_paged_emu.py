@@ -216,6 +216,25 @@ def test_decode_infinite_values(emu, D, G, Tq):
         assert (decode_raw(emu, q[:, :, -1:], k, v, table, 1, grid, scale)[0] == np.inf).all()
 
 
+@pytest.mark.parametrize("D,G,Tq", [(64, 1, 1), (128, 9, 1), (32, 3, 2)])
+def test_decode_large_values(emu, D, G, Tq):
+    """scores that rise by less than the running maximum follows, with values
+    near the largest bf16: finite where the formula is"""
+    L, P, n = 131 + Tq, 16, 9
+    table = np.arange(n, dtype=np.int32)[None]
+    k, v, q = rows(1, n, 1, P, D), rows(2, n, 1, P, D), rows(3, 1, G, Tq, D, std=1.5)
+    q[..., 0], k[..., 0] = 1, 0
+    q[..., 1:] = 0
+    for pos, x in ((128, 5.25), (129, 5.5), (130, 5.375)):      # e^5.5 < 2^8
+        k[table[0, pos // P], 0, pos % P, 0] = x
+        v[table[0, pos // P], 0, pos % P, :] = 3e38 * (-1) ** pos
+        v[table[0, pos // P], 0, pos % P, 1::2] = 1.5e38
+    ref = opaged.decode(as64(q), as64(k), as64(v), table, [L], 1.0)
+    for grid in (1, 2, -1, -2):
+        o, lse = decode_raw(emu, q, k, v, table, L, grid, 1.0)
+        check_decode(o, lse, ref, L, D)
+
+
 @pytest.mark.parametrize("Tq,G", [(1, 1), (2, 3)])
 def test_sparse(emu, Tq, G):
     pages = np.full((3, 2, 4), -1)
