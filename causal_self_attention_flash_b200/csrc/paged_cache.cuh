@@ -572,7 +572,7 @@ __host__ __device__ constexpr int score_ring_bytes(int D) { return kScoreStages 
 // k-steps (the channels of a segment enter the product in the order that this
 // gives, on both sides).  The page numbers of four groups are looked up at a
 // time, one per lane, ahead of their use.  UP: more than 8 query rows.
-// Returns the largest |bound|.
+// Returns the largest |bound|, infinity where one is NaN.
 template <int D, bool UP>
 __device__ __forceinline__ float score_groups(const SelectParams& p, int b, int h, int count,
                                               int first, int end, int step, uint8_t* ring) {
@@ -683,6 +683,8 @@ __device__ __forceinline__ float score_groups(const SelectParams& p, int b, int 
     dec_cp_async_wait<0>();
   }
   float big = fmaxf(dec_bf16_lo(big2), dec_bf16_hi(big2));
+  // a NaN outranks every number in big2 and may hide the largest
+  if ((big2 & 0xffffu) > 0x7f80u || (big2 >> 16) > 0x7f80u) big = INFINITY;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
   return big;

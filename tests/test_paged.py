@@ -343,6 +343,32 @@ def test_select_ties_nan_and_pages_that_are_not_held(lib):
     check(q, bounds, table)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_select_nan_in_a_page_that_is_always_taken(lib, bad):
+    """NaN or infinite bounds of the first page: the others are chosen by their
+    exact sums all the same, here pairs whose terms of 2^20 cancel"""
+    P, D, Hkv, L = 4, 64, 16, 1200
+    q, bounds, table = select_inputs(5, [L], Hkv, 1, 1, D, P)
+    q[:] = 1
+    bounds[:] = bounds.clamp(-0.01, 0.01)
+    bounds[:, :, 1] = 0
+    bounds[table[0, 0]] = bad
+    for page in range(8, 300, 8):
+        x = rows(page, Hkv, 5).abs() / 16
+        for h in range(Hkv):
+            hi = bounds[table[0, page], h, 1]
+            hi[0], hi[40] = 2.0 ** 20, -2.0 ** 20
+            hi[[3, 5, 18, 21, 30]] = x[h]
+    tb, ln = dev(table), dev([L])
+    wide = torch.full((1, 20000), -1, dtype=torch.int32, device=DEV)   # two launches
+    wide[:, :table.shape[1]] = tb
+    for K in (2, 9):
+        want = opaged.select(as64(q), as64(bounds), table, [L], P, K, 1, 0)
+        for t in (tb, wide):
+            got = lib.attn_page_select(q.to(DEV), bounds.to(DEV), t, ln, P, K, n_last=0)
+            assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_select_sure_pages_beside_ties(lib):
     """sure pages in several warps and ties at the border, many heads at once
     and again and again: the choice is the oracle's each time"""

@@ -453,3 +453,21 @@ def test_select_with_a_late_warp(emu, monkeypatch, groups, gap):
             bounds[table[0, i]] *= gap
         bounds[:, :, 0] = 0
     run_select(emu, [320], 1, 1, 1, 16, 4, 45, change=change, groups=groups)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_select_nan_in_a_page_that_is_always_taken(emu, bad):
+    """NaN or infinite bounds of the first page: the others are chosen by their
+    exact sums all the same, here two whose terms of 2^20 cancel"""
+    for seed in range(6):
+        def change(q, bounds, table):
+            q[:] = 1
+            bounds[:] = bounds.clamp(-0.01, 0.01)
+            bounds[:, :, 1] = 0
+            bounds[table[0, 0]] = bad
+            x = rows(seed + 50, 2, 5).abs()
+            for i, page in ((0, 8), (1, 16)):
+                hi = bounds[table[0, page], 0, 1]
+                hi[0], hi[40] = 2.0 ** 20, -2.0 ** 20
+                hi[[3, 5, 18, 21, 30]] = x[i] / 16
+        run_select(emu, [120], 1, 1, 1, 64, 4, 2, n_last=0, change=change, seed=seed, groups=3)
