@@ -825,12 +825,14 @@ cattn_status paged_decode(const void* q, cattn_layout lq, const void* k, cattn_l
   const long long keys = static_cast<long long>(pages ? n_sel : width) * P;
   if (keys > (1LL << 30) || rows > (1LL << 20)) return CATTN_ERR_INVALID_ARG;
   const long long chunks = (keys + paged_chunk(D) - 1) / paged_chunk(D);
-  if (B * chunks > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
+  // places on the flat axis: 32 bits for a head's, and a CTA's share of all
+  const long long places = B * (chunks + paged_item_cost(D));
+  if (places > 0x7fffffffLL) return CATTN_ERR_INVALID_ARG;
   PagedParams p;
   p.rows = static_cast<int>(rows);
   p.n_tiles = (p.rows + kPagedRows - 1) / kPagedRows;
   p.R = p.rows < kPagedRows ? p.rows : kPagedRows;
-  if (B * chunks > (1LL << 38) / (static_cast<long long>(Hkv) * p.n_tiles))
+  if (places > (1LL << 38) / (static_cast<long long>(Hkv) * p.n_tiles))
     return CATTN_ERR_INVALID_ARG;
   if (workspace_bytes < static_cast<size_t>(paged_workspace_bytes(p.R, D)))
     return CATTN_ERR_INVALID_ARG;

@@ -430,8 +430,8 @@ CATTN_API cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, co
  * tables have room for short requests only, else two; results do not depend on
  * the run.  Errors: CATTN_ERR_INVALID_ARG (as attn_decode;
  * Hkv, page_size, width or table_stride out of range; tables with room for
- * 2^31 or more chunks of 32 keys, 16 at D = 128, or over 2^38 for all heads; a small or misaligned
- * workspace), CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  B = 0 or H = 0 is a
+ * 2^31 or more chunks of 32 keys (16 at D = 128), counting 4 (2) more for each
+ * request, or for over 2^38 with all heads; a small or misaligned workspace), CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  B = 0 or H = 0 is a
  * no-op. */
 CATTN_API size_t attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int Tq, int D);
 

@@ -50,6 +50,25 @@ def test_decode_refuses_more_chunks_than_it_counts():
     assert decode(B=1, H=1 << 21, Hkv=1) == INVALID
 
 
+def test_decode_counts_what_a_request_costs_beside_its_chunks():
+    """the places of a request on the flat axis are its chunks and 4 (2 at D =
+    128) more: their sum has to fit 32 bits, and 2^38 for all heads"""
+    if torch.cuda.is_available():
+        pytest.skip("the calls that are not refused would run")
+    wide = dict(P=32, n_pages=9)                # D = 64: a page is a chunk
+
+    def refused(B, width, **kw):
+        return decode(B=B, width=width, stride=width, **{**wide, **kw}) == INVALID
+    assert refused(64, (1 << 25) - 1) and refused(64, (1 << 25) - 4)
+    assert not refused(64, (1 << 25) - 5)
+    big = dict(D=128, P=16, lq=L(512, 128, 128), lo=L(512, 128, 128), lk=L(4096, 128, 256),
+               lv=L(4096, 128, 256))
+    assert refused(64, (1 << 25) - 2, **big) and not refused(64, (1 << 25) - 3, **big)
+    heads = dict(H=1 << 12, Hkv=1 << 12, lq=L(1 << 18, 64, 64), lo=L(1 << 18, 64, 64),
+                 lk=L(1 << 23, 64, 1 << 18), lv=L(1 << 23, 64, 1 << 18))
+    assert refused(2, (1 << 25) - 3, **heads) and not refused(2, (1 << 25) - 4, **heads)
+
+
 @pytest.mark.parametrize("sparse", [False, True])
 def test_decode_unsupported_and_empty(sparse):
     assert decode(sparse, D=48) == UNSUPPORTED
