@@ -8,10 +8,15 @@ missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.metadata
+import importlib.util
 import os
 import struct
+import sys
+import warnings
 
-import torch  # noqa: F401  (before _torch_calls, which links against its libraries)
+import torch  # noqa: F401  (before the marshalling, which links against its libraries)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcattn.so")
@@ -132,17 +137,34 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 LIB = load()
 
 
+class LongWay:
+    """Stands in for the marshalling of the paged calls: it recognises no
+    arguments, so every call goes through the Python wrapper."""
+
+    @staticmethod
+    def _unknown(*args):
+        return -1
+    decode = append = plan = select = _unknown
+
+
 def load_torch_calls():
     """The marshalling of the paged calls (csrc/torch_calls.cpp), set to make
-    them through this process's libcattn."""
+    them through this process's libcattn; LongWay where there is none for this
+    Python and torch (the library itself needs neither)."""
+    path = os.path.join(HERE, f"_torch_calls-{sys.implementation.cache_tag}-"
+                              f"torch{importlib.metadata.version('torch')}.so")
     try:
-        from . import _torch_calls
+        loader = importlib.machinery.ExtensionFileLoader(__package__ + "._torch_calls", path)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location(loader.name, path, loader=loader))
+        loader.exec_module(module)
     except ImportError as e:
-        raise ImportError(
-            f"_torch_calls.so is missing or was built for another torch ({e}); build it with "
-            "`python causal_self_attention_flash_b200/build.py`") from e
-    _torch_calls.use(ctypes.cast(LIB.attn_paged_call, ctypes.c_void_p).value)
-    return _torch_calls
+        warnings.warn(f"{os.path.basename(path)} cannot be loaded ({e}): the paged calls take some "
+                      "microseconds longer; build it with "
+                      "`python causal_self_attention_flash_b200/build.py`", RuntimeWarning)
+        return LongWay()
+    module.use(ctypes.cast(LIB.attn_paged_call, ctypes.c_void_p).value)
+    return module
 
 
 TORCH_CALLS = load_torch_calls()

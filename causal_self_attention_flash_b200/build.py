@@ -1,13 +1,16 @@
-"""Build libcattn.so (sm_100a) in-tree with nvcc, and _torch_calls.so, the
+"""Build libcattn.so (sm_100a) in-tree with nvcc, and _torch_calls-*.so, the
 Python binding's argument marshalling, with the host compiler.
 
     python causal_self_attention_flash_b200/build.py [--force]
 
-Both land next to this file, so they travel with the source tree.
+Both land next to this file, so they travel with the source tree.  The second
+holds for one Python and one torch, which its name tells; the package does
+without it, at some microseconds a call.
 """
 
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -18,8 +21,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcattn.so")
-
-BINDING = os.path.join(HERE, "_torch_calls.so")
 
 SOURCES = ["api.cu"]
 BINDING_SOURCE = "torch_calls.cpp"
@@ -50,13 +51,21 @@ def _stale() -> bool:
     return any(os.path.getmtime(f) > t for f in files)
 
 
+def binding_path() -> str:
+    """Where the binding for this Python and the installed torch is (_binding.py
+    looks for the same name)."""
+    torch_version = importlib.metadata.version("torch")
+    return os.path.join(
+        HERE, f"_torch_calls-{sys.implementation.cache_tag}-torch{torch_version}.so")
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """_torch_calls.so, against the headers of the installed torch."""
-    src = os.path.join(CSRC, BINDING_SOURCE)
+    """The binding, against the headers of the installed torch."""
+    src, out = os.path.join(CSRC, BINDING_SOURCE), binding_path()
     files = [src, os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and \
-            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in files):
-        return BINDING
+    if not force and os.path.exists(out) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(out) for f in files):
+        return out
     import sysconfig
 
     import torch
@@ -67,24 +76,23 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(cuda, "include"), src, "-L", lib, f"-Wl,-rpath,{lib}",
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", BINDING + ".tmp"]
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", out + ".tmp"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(BINDING + ".tmp", BINDING)
-    return BINDING
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    if force or _stale():
+        cmd = [nvcc_path(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC,
+               *[os.path.join(CSRC, s) for s in SOURCES], "-o", LIB + ".tmp"]
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.run(cmd, check=True)
+        os.replace(LIB + ".tmp", LIB)
     build_binding(force, verbose)
-    if not force and not _stale():
-        return LIB
-    cmd = [nvcc_path(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", LIB + ".tmp"]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 
