@@ -18,9 +18,9 @@ namespace cattn {
 //   have = ceil(length / P), need = ceil((length + n) / P) - have,
 // and exclusive sums over the requests, new page j of request b is
 // ring[head + sum need + j], its token i has position length + i and slot
-// table[b][pos / P] P + pos % P, and the pages of the requests that end go to
-// ring[tail + sum have ..].  A call that cannot be served as a whole
-// changes nothing but its status.
+// table[b][pos / P] P + pos % P, and the held pages of the requests that end go
+// to ring[tail ..] in order: at sum have + j where all are held.  A call that
+// cannot be served as a whole changes nothing but its status.
 //
 // A few kilobytes of whole numbers: bound by latency.  One thread-block
 // cluster: every CTA scans all requests for itself (into shared
@@ -162,11 +162,11 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   int status = 0;
   if (T > p.n_slots || N > avail) status = kPlanStatusTooLarge;
   if (bad[2]) status = kPlanStatusTooLarge;
-  if (bad[1] || head < 0 || avail < 0 || avail > p.n_pages || R > p.n_pages - avail)
+  if (bad[1] || head < 0 || avail < 0 || avail > p.n_pages || R > 0x7fffffffLL)
     status = kPlanStatusInvalid;
   for (int b = b0; b < b1; ++b) {
     const int len = p.lengths[b], n = p.asked[b];
-    len_s[b] = status || n >= 0 ? len : -1;  // -1: the request ends
+    len_s[b] = status || n >= 0 ? len : ~len;  // below 0: the request ends
     cu_tok[b] = status ? 0 : static_cast<int>(et);
     cu_need[b] = status ? 0 : static_cast<int>(en);
     cu_back[b] = status ? 0 : static_cast<int>(eb);
@@ -183,9 +183,72 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     cu_back[p.B] = static_cast<int>(R);
   }
   __syncthreads();
-  if (n_ctas > 1) dec_cluster_sync();  // every CTA has read its inputs
-
+  // Entry j of the rows of the requests that end.
+  auto ended = [&](long long j) {
+    const int b = last_at_most(cu_back, 0, p.B, static_cast<int>(j));
+    return p.table[b * p.table_sb + (j - cu_back[b])];
+  };
+  auto held = [&](int page) { return page >= 0 && page < p.n_pages; };
+  // Where some are not held: f(rank, page, tile) for each held one, a tile of nt
+  // entries at a time (every CTA walks all of them); returns their number.
+  auto each_held = [&](auto f) {
+    long long rank_in = 0;
+    for (long long base = 0, tile = 0; base < R; base += nt, ++tile) {
+      const int page = base + tid < R ? ended(base + tid) : -1;
+      const unsigned m = dec_ballot(held(page));
+      __syncthreads();  // the tile before is done with the counts
+      if (lane == 0) sums[warp * 4] = dec_popc(m);
+      __syncthreads();
+      long long at = rank_in + dec_popc(m & ((1u << lane) - 1u));
+      for (int w = 0; w < nw; ++w) {
+        if (w < warp) at += sums[w * 4];
+        rank_in += sums[w * 4];
+      }
+      if (held(page)) f(at, page, tile);
+    }
+    return rank_in;
+  };
+  constexpr int ILP = 4;  // entries in flight per thread
   const int start = static_cast<int>(rank) * nt + tid, step = n_ctas * nt;
+  // whether there are any: each CTA looks at its share, of which the first
+  // entries stay in registers
+  const bool ending = R > 0;  // (alike in every CTA)
+  int first[ILP];
+  for (long long j0 = start; j0 < R; j0 += ILP * step) {
+    int entry[ILP];
+#pragma unroll
+    for (int u = 0; u < ILP; ++u) entry[u] = j0 + u * step < R ? ended(j0 + u * step) : 0;
+#pragma unroll
+    for (int u = 0; u < ILP; ++u) {
+      if (!held(entry[u])) bad[3] = 1;
+      if (j0 == start) first[u] = entry[u];
+    }
+  }
+  if (n_ctas > 1)
+    dec_cluster_sync();  // every CTA has read its inputs
+  else
+    __syncthreads();
+  bool holes = false;
+  if (ending) {
+    const float* flag = reinterpret_cast<const float*>(bad + 3);
+    holes = n_ctas > 1
+                ? dec_ballot(lane < n_ctas && dec_float_bits(dec_cluster_ld(flag, lane)) != 0u) != 0u
+                : bad[3] != 0;
+    const long long n_held = holes ? each_held([](long long, int, long long) {}) : R;
+    if (n_held > p.n_pages - avail) {  // (every thread of every CTA finds the same)
+      status = kPlanStatusInvalid;
+      __syncthreads();
+      for (int b = b0; b < b1; ++b) {
+        if (len_s[b] < 0) len_s[b] = ~len_s[b];
+        cu_tok[b] = cu_need[b] = cu_back[b] = 0;
+      }
+      T = N = R = 0;
+      if (tid == 0) cu_tok[p.B] = cu_need[p.B] = cu_back[p.B] = 0;
+      holes = false;
+      __syncthreads();
+    }
+  }
+
   const int head0 = static_cast<int>(head % p.n_pages >= 0 ? head % p.n_pages : 0);
   const int tail0 = static_cast<int>(tail % p.n_pages >= 0 ? tail % p.n_pages : 0);
   auto at = [&](int base, int k) {  // ring entry of counter base + k, k < n_pages
@@ -211,37 +274,32 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     p.positions[i] = pos;
   }
   // new pages into the table, freed ones into the ring, four at a time
-  constexpr int ILP = 4;
-  for (int j0 = start; j0 < N; j0 += ILP * step) {
+  for (long long j0 = start; j0 < N; j0 += ILP * step) {
     int entry[ILP];
 #pragma unroll
     for (int u = 0; u < ILP; ++u) {
-      const long long j = j0 + static_cast<long long>(u) * step;
+      const long long j = j0 + u * step;
       entry[u] = j < N ? p.ring[at(head0, static_cast<int>(j))] : -1;
     }
 #pragma unroll
     for (int u = 0; u < ILP; ++u) {
-      const long long j = j0 + static_cast<long long>(u) * step;
+      const long long j = j0 + u * step;
       if (j >= N) continue;
       const int b = last_at_most(cu_need, 0, p.B, static_cast<int>(j));
       p.table[b * p.table_sb + pages(len_s[b]) + (j - cu_need[b])] = entry[u];
     }
   }
-  for (int j0 = start; j0 < R; j0 += ILP * step) {
-    int entry[ILP];
+  if (holes) {
+    R = each_held([&](long long j, int page, long long tile) {
+      if (tile % n_ctas == rank) p.ring[at(tail0, static_cast<int>(j))] = page;
+    });
+  } else {
+    for (long long j0 = start; j0 < R; j0 += ILP * step) {
 #pragma unroll
-    for (int u = 0; u < ILP; ++u) {
-      const long long j = j0 + static_cast<long long>(u) * step;
-      entry[u] = -1;
-      if (j < R) {
-        const int b = last_at_most(cu_back, 0, p.B, static_cast<int>(j));
-        entry[u] = p.table[b * p.table_sb + (j - cu_back[b])];
+      for (int u = 0; u < ILP; ++u) {
+        const long long j = j0 + u * step;
+        if (j < R) p.ring[at(tail0, static_cast<int>(j))] = j0 == start ? first[u] : ended(j);
       }
-    }
-#pragma unroll
-    for (int u = 0; u < ILP; ++u) {
-      const long long j = j0 + static_cast<long long>(u) * step;
-      if (j < R) p.ring[at(tail0, static_cast<int>(j))] = entry[u];
     }
   }
   for (int b = start; b <= p.B; b += step) {
@@ -254,6 +312,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     p.state_out[1] = tail + R;
     p.status[0] = status;
   }
+  if (n_ctas > 1 && ending) dec_cluster_sync();  // no CTA leaves while its flag is read
 }
 
 // Slots and positions of a planned step's tokens, from what the plan wrote:

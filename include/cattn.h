@@ -347,8 +347,8 @@ CATTN_API cattn_status attn_decode(const void* q, cattn_layout lq, const void* k
 /* Plan of a step: gives the new tokens their pages, slots and positions.
  *
  *   new_tokens  int32 (B): tokens that request b adds; 0: none; negative:
- *               the request ends and its pages become free (its new length
- *               is 0; its row of the table is left as it is)
+ *               the request ends and the pages that it holds become free (its
+ *               new length is 0; its row of the table is left as it is)
  *   lengths     int32 (B): positions that are cached
  *   block_table int32 (B, width), in/out: entries of new pages are written
  *   free_ring   int32 (n_pages), in/out, and ring_state int64 (2) = { head,

@@ -167,8 +167,9 @@ def plan(asked, lengths, table, ring, state, P, n_slots):
             out.append(length + n)
         elif n < 0:
             for i in range(n_pages_of(length, P)):
-                new_ring[(tail + freed) % n_pool] = table[b, i]
-                freed += 1
+                if 0 <= table[b, i] < n_pool:       # a page that is held
+                    new_ring[(tail + freed) % n_pool] = table[b, i]
+                    freed += 1
             out.append(0)
         else:
             out.append(length)

@@ -254,6 +254,29 @@ def test_plan(lib, B, P, longest, most, in_place):
     assert np.array_equal(rg.cpu().numpy(), want["ring"])
 
 
+@pytest.mark.parametrize("B,longest", [(40, 100), (3000, 600)])
+def test_plan_frees_held_pages_only(lib, B, longest):
+    """entries that are not held in the rows of requests that end do not get
+    into the ring"""
+    P = 8
+    asked, lengths, table, ring, state = plan_inputs(12, B, P, longest, 2)
+    rng = np.random.default_rng(1)
+    for b in np.flatnonzero(asked < 0)[::2]:
+        for i in rng.integers(0, table.shape[1], 5):
+            table[b, i] = rng.choice([-1, len(ring), 2 ** 31 - 1, -2 ** 31])
+    n_slots = int(np.maximum(asked, 0).sum())
+    want = opaged.plan(asked, lengths, table, ring, state, P, n_slots)
+    tb, rg = dev(table), dev(ring)
+    got = lib.attn_paged_plan(dev(asked), dev(lengths), tb, rg, dev(state, torch.int64), P, n_slots)
+    for key, x in zip(("lengths", "state", "cu", "slots", "positions"), got):
+        assert np.array_equal(x.cpu().numpy(), want[key]), key
+    assert int(got[5]) == want["status"] == opaged.OK
+    assert np.array_equal(tb.cpu().numpy(), want["table"])
+    assert np.array_equal(rg.cpu().numpy(), want["ring"])
+    assert want["state"][1] - state[1] < sum(opaged.n_pages_of(n, P)
+                                             for n, a in zip(lengths, asked) if a < 0)
+
+
 def test_plan_refuses_as_a_whole(lib):
     asked, lengths, table, ring, state = plan_inputs(3, 40, 8, 50, 20)
     n = int(np.maximum(asked, 0).sum())

@@ -333,6 +333,40 @@ def test_plan_without_requests_and_with_foreign_pages(emu):
     assert (want["slots"] == -1).any() and (want["slots"] >= 0).any()
 
 
+@pytest.mark.parametrize("ctas,threads,prompts", [(1, 256, False), (3, 64, False), (2, 128, True)])
+def test_plan_frees_held_pages_only(emu, ctas, threads, prompts):
+    """entries that are not held in the rows of requests that end: they are not
+    put into the ring, and none is handed out afterwards"""
+    B, P = 30, 4
+    asked, lengths, table, ring, state = plan_inputs(11, B, P, 90, 3)
+    asked = np.maximum(asked, 0)
+    asked[::3], lengths[::3] = -1, np.maximum(lengths[::3], 5)
+    for b in range(B):
+        for i in range(opaged.n_pages_of(lengths[b], P), table.shape[1]):
+            table[b, i] = -1
+    for j, bad in enumerate((-1, len(ring), -2 ** 31, 2 ** 31 - 1, -1, -1)):
+        table[6 * (j % 5), j % 2] = bad
+    table[27, :2] = -1                              # a row without a held page in front
+    n_slots = int(np.maximum(asked, 0).sum()) + 3
+    want = run_plan(emu, asked, lengths, table, ring, state, P, n_slots, ctas, False, threads,
+                    prompts)
+    assert want["status"] == opaged.OK
+    head, tail = want["state"]
+    assert all(0 <= want["ring"][i % len(ring)] < len(ring) for i in range(head, tail))
+    # more of them held than the ring has room for: refused, nothing changed
+    many = table.copy()
+    many[::3, :2] = 0
+    want = run_plan(emu, asked, lengths, many, ring, np.array([0, len(ring)]), P, n_slots, ctas,
+                    False, threads, prompts)
+    assert want["status"] == opaged.INVALID
+    # entries that are not held take no room
+    none = table.copy()
+    none[::3] = -1
+    want = run_plan(emu, asked, lengths, none, ring, np.array([0, len(ring)]), P, n_slots, ctas,
+                    False, threads, prompts)
+    assert want["status"] == opaged.OK
+
+
 # ----------------------------------------------------------------- append
 
 def run_append(emu, slots, Hkv, D, n_pages, P, bounds=True, bad=None, seed=0, tile=1):

@@ -104,8 +104,16 @@ def pin_plan_by_hand(m):
     assert few["status"] == m.TOO_LARGE and few["lengths"].tolist() == [5, 2, 0, 1]
 
 
+def pin_plan_frees_held_pages_only(m):
+    holed = np.array([[4, 0, -1], [6, 2, -1], [-1, -1, -1], [3, -1, -1]])
+    got = m.plan([0, -1, 0, 0], [5, 6, 0, 1], holed, np.array([9, 1, 5, 4, 3, 8]), [1, 4], 3, 6)
+    assert got["status"] == m.OK and got["state"].tolist() == [1, 5]
+    assert got["ring"].tolist() == [9, 1, 5, 4, 2, 8] and got["lengths"].tolist() == [5, 0, 0, 1]
+
+
 ALL_PINS = [pin_rows_of_full_attention, pin_rows_without_keys, pin_listed_pages,
-            pin_select_bounds_the_scores, pin_append_keeps_lowest_and_highest, pin_plan_by_hand]
+            pin_select_bounds_the_scores, pin_append_keeps_lowest_and_highest, pin_plan_by_hand,
+            pin_plan_frees_held_pages_only]
 
 
 @pytest.mark.parametrize("pin", ALL_PINS, ids=lambda p: p.__name__)
@@ -124,6 +132,8 @@ MUTANTS = [
     ("last pages not forced", "set(range(n - n_last, n))", "set()"),
     ("old bounds kept", "if row == 0:", "if row < 0:"),
     ("ring's entries in reverse", "ring[(head + taken) % n_pool]", "ring[(tail - 1 - taken) % n_pool]"),
+    ("pages that are not held freed", "if 0 <= table[b, i] < n_pool:       # a page that is held",
+     "if True:"),
     ("freed to the head", "new_ring[(tail + freed) % n_pool]", "new_ring[(head + freed) % n_pool]"),
 ]
 
