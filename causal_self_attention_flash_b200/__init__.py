@@ -670,6 +670,9 @@ def attn_decode_sparse(q, k_cache, v_cache, block_table, lengths, pages, scale=N
                        lse=None, workspace=None, stream=None):
     """attn_decode_paged over the listed pages only: pages int32 (B, Hkv, K)
     as attn_page_select gives them."""
+    if pages is None or len(pages.shape) != 3:
+        raise ValueError("pages: expected an int32 (B, Hkv, K) tensor, got "
+                         f"{None if pages is None else tuple(pages.shape)}")
     return _decode_paged(CALL_DECODE_SPARSE, q, k_cache, v_cache, block_table, lengths, pages,
                          scale, o, lse, workspace, stream)
 

@@ -238,6 +238,23 @@ def test_binding_refuses_before_the_call(fake):
     assert fake.calls == []
 
 
+def test_sparse_needs_its_lists(fake, monkeypatch):
+    """attn_decode_sparse without lists is refused; the marshalling never sees
+    it (there, no lists means the dense call)"""
+    class Dense:
+        def decode(self, *args):
+            return 0
+    monkeypatch.setattr(cattn, "TORCH_CALLS", Dense())
+    q, k = dev(2, 4, 1, 64), dev(9, 2, 16, 64)
+    t, n = dev(2, 5, dtype=torch.int32), dev(2, dtype=torch.int32)
+    o, lse, ws = dev(2, 4, 1, 64), dev(2, 4, 1, dtype=torch.float32), dev(99, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="pages"):
+        cattn.attn_decode_sparse(q, k, k, t, n, None, 1.0, o, lse, ws)
+    with pytest.raises(ValueError, match="pages"):
+        cattn.attn_decode_sparse(q, k, k, t, n, dev(2, 6, dtype=torch.int32))
+    assert fake.calls == []
+
+
 def test_binding_needs_the_current_device(fake, monkeypatch):
     monkeypatch.setattr(cattn.torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="current device"):
