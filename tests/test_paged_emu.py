@@ -505,3 +505,41 @@ def test_select_nan_in_a_page_that_is_always_taken(emu, bad):
                 hi[0], hi[40] = 2.0 ** 20, -2.0 ** 20
                 hi[[3, 5, 18, 21, 30]] = x[i] / 16
         run_select(emu, [120], 1, 1, 1, 64, 4, 2, n_last=0, change=change, seed=seed, groups=3)
+
+
+# ------------------------- forms that the parameters above leave out
+
+@pytest.mark.parametrize("lengths,Hkv,G,Tq,P,ctas", [
+    ([70, 3], 1, 2, 1, 16, 1), ([45], 1, 9, 2, 16, 2), ([130], 2, 3, 2, 20, 2),
+    ([0, 33], 1, 16, 1, 8, 1)])
+def test_decode_an_item_per_cluster_d128(emu, lengths, Hkv, G, Tq, P, ctas):
+    run_decode(emu, lengths, Hkv, G, Tq, 128, P, -ctas, spare=1, seed=3)
+
+
+def test_decode_many_requests_of_some_chunks(emu):
+    """several requests per thread of the scan, of one to three chunks each"""
+    run_decode(emu, [(i * 37) % 90 for i in range(140)], 1, 1, 1, 16, 8, 2)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_prompts(emu, in_place):
+    asked, lengths, table, ring, state = plan_inputs(8, 9, 5, 33, 200)
+    n_slots = int(np.maximum(asked, 0).sum()) + 3
+    run_plan(emu, asked, lengths, table, ring, state, 5, n_slots, 2, in_place, 64, True)
+
+
+@pytest.mark.parametrize("D,tile", [(16, 1), (64, 4), (128, 1), (128, 4), (32, 32)])
+def test_append_tiles(emu, D, tile):
+    slots = [21, 22, 23, 24, 25, 40, -1, 3, 10 ** 12, 8, 9, 50, 55, -2 ** 62]
+    run_append(emu, slots, 3, D, 8, 8, True, tile=tile)
+    if tile == 1:
+        run_append(emu, list(range(7, 60)), 2, D, 3, 20, tile=1)
+
+
+@pytest.mark.parametrize("ties", [False, True])
+def test_select_in_one_launch(emu, ties):
+    def same(q, bounds, table):
+        bounds[:] = bounds[:1]
+        bounds[::2, :, :, 3:5] *= -1            # zeros of both signs among them
+        q[..., 3:5] = 0
+    run_select(emu, [300, 21], 1, 2, 1, 128, 4, 9, change=same if ties else None, seed=6)
