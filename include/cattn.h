@@ -397,9 +397,11 @@ CATTN_API cattn_status attn_paged_plan(const int32_t* new_tokens, const int32_t*
  *                 in, NaN out.
  *
  * With bounds, the tokens of a page must be neighbours in the list (as in the
- * plan); they are then written one after another.  Otherwise slots must
- * differ.  A list that breaks this leaves either token's row (and bounds) in
- * the page concerned.  The inputs must not overlap the cache.  Errors:
+ * plan, with no skipped one between them); they are then written one after
+ * another, the last of the same slot stays.  Otherwise slots must differ.  A
+ * list that breaks this leaves a mix of the tokens' rows, 16 bytes from one or
+ * the other (and bounds that may lack one of them) in the page concerned.  The
+ * inputs must not overlap the cache.  Errors:
  * CATTN_ERR_INVALID_ARG (a cache layout that overlaps itself included),
  * CATTN_ERR_UNSUPPORTED, CATTN_ERR_CUDA.  n = 0 is a no-op. */
 CATTN_API cattn_status attn_cache_append(const void* k_new, cattn_layout lkn, const void* v_new,
@@ -454,7 +456,9 @@ CATTN_API cattn_status attn_decode_paged(const void* q, cattn_layout lq, const v
  * n = min(ceil(lengths[b] / page_size), width) pages the n_first first and
  * n_last last are taken, then those of the highest s_i (the lower index
  * where equal; a page that is not held last, a NaN first) up to n_select, or
- * all n if there are no more.  The scores are compared as exact sums.
+ * all n if there are no more.  The scores are compared as sums in 64 bits,
+ * which are exact where a sum's terms span less than 2^29: the choice does not
+ * depend on an order of summation.
  *
  *   bounds  bf16 (n_pages, Hkv, 2, D) contiguous (attn_cache_append)
  *   pages   int32 (B, Hkv, n_select) out: indices into the request's row of

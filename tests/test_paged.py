@@ -211,6 +211,17 @@ def test_strides_outputs_and_repeats(lib):
     assert torch.equal(o2, o) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("lengths,G,Tq,D", [([300, 41], 2, 1, 64), ([9000], 3, 2, 128)])
+def test_k_and_v_in_different_layouts(lib, lengths, G, Tq, D):
+    q, k, v, kd, vd, table = setup(14, lengths, 2, G, Tq, D, 16)
+    gaps = torch.full((k.shape[0], 2, 16 + 3, D + 8), float("nan"), dtype=torch.bfloat16, device=DEV)
+    gaps[:, :, :16, :D] = v.to(DEV)
+    ref = opaged.decode(as64(q), as64(k), as64(v), table, lengths, np.float32(D ** -0.5))
+    for kk, vv in ((kd, v.to(DEV)), (k.to(DEV), vd), (kd, gaps[:, :, :16, :D])):
+        o, lse = lib.attn_decode_paged(q.to(DEV), kk, vv, dev(table), dev(lengths))
+        check_decode(as64(o.cpu()), as64(lse.cpu()), ref, max(lengths), D)
+
+
 def test_offsets_beyond_32_bits(lib):
     """a pool of more than 2^32 elements, read and written at its far end"""
     P, D, Hkv = 64, 128, 8
@@ -501,6 +512,36 @@ def test_a_server_run(lib):
     free = int(s.state[1] - s.state[0])
     held = sum(opaged.n_pages_of(len(x), 8) for x in s.seen)
     assert free + held == 40
+
+
+def test_packed_steps(lib):
+    """requests that bring prompts, go on, idle and end in one step: the plan's
+    packed rows, and the newest of each request for the attention"""
+    B, Hkv, G, D, P, n_pages, width = 6, 2, 2, 64, 8, 60, 20
+    s = Server(lib, B, Hkv, G, D, P, n_pages, width, seed=500)
+    for i, asked in enumerate(([20, 0, 7, 1, 0, 33], [1, 12, 0, -1, 9, 1], [0, 1, 1, 5, -1, 1],
+                               [-1, 1, 0, 1, 0, 2])):
+        total = sum(max(n, 0) for n in asked)
+        q_new = rows(600 + i, total, Hkv * G, D, std=1.5)
+        kn, vn = rows(700 + i, total, Hkv, D), rows(800 + i, total, Hkv, D)
+        at = 0
+        for b, n in enumerate(asked):
+            s.seen[b] = [] if n < 0 else s.seen[b] + [(kn[at + j], vn[at + j]) for j in range(n)]
+            at += max(n, 0)
+        _, _, cu_new, slots, _, status = lib.attn_paged_plan(
+            dev(asked), s.lengths, s.table, s.ring, s.state, P, total, lengths_out=s.lengths,
+            ring_state_out=s.state)
+        lib.attn_cache_append(kn.to(DEV), vn.to(DEV), s.pool[0], s.pool[1], slots, s.bounds)
+        newest = (cu_new[1:] - 1).clamp(min=0).long()
+        q = q_new.to(DEV)[newest].unsqueeze(2)
+        o, lse = lib.attn_decode_paged(q, s.pool[0], s.pool[1], s.table, s.lengths)
+        torch.cuda.synchronize()
+        assert int(status) == 0
+        ends = np.cumsum([max(n, 0) for n in asked]) - 1
+        for b, n in enumerate(asked):
+            if n > 0:
+                assert torch.equal(q[b, :, 0].cpu(), q_new[ends[b]])
+        s.check(q.cpu(), o, lse, None)
 
 
 def test_a_captured_step(lib):
