@@ -467,7 +467,8 @@ def attn_decode(q, k, v, L, scale=None, o=None, lse=None, workspace=None, stream
 # cost in Python counts.  On the current stream and with the outputs given,
 # TORCH_CALLS reads the tensors and makes the call (1 us before the launch);
 # what it does not recognise (-1) goes the long way below, which says what is
-# wrong or makes the call itself (7 us).
+# wrong or makes the call itself (10 us a call with its launch against 4 to 5;
+# 20 where it also allocates outputs and workspace).
 
 _BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
 
