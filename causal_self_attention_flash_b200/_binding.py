@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import importlib.machinery
-import importlib.metadata
 import importlib.util
 import os
 import struct
@@ -152,7 +151,7 @@ def load_torch_calls():
     them through this process's libcattn; LongWay where there is none for this
     Python and torch (the library itself needs neither)."""
     path = os.path.join(HERE, f"_torch_calls-{sys.implementation.cache_tag}-"
-                              f"torch{importlib.metadata.version('torch')}.so")
+                              f"torch{torch.__version__}.so")
     try:
         loader = importlib.machinery.ExtensionFileLoader(__package__ + "._torch_calls", path)
         module = importlib.util.module_from_spec(

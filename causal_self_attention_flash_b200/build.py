@@ -10,7 +10,6 @@ without it, at some microseconds a call.
 
 from __future__ import annotations
 
-import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -54,9 +53,9 @@ def _stale() -> bool:
 def binding_path() -> str:
     """Where the binding for this Python and the installed torch is (_binding.py
     looks for the same name)."""
-    torch_version = importlib.metadata.version("torch")
+    import torch
     return os.path.join(
-        HERE, f"_torch_calls-{sys.implementation.cache_tag}-torch{torch_version}.so")
+        HERE, f"_torch_calls-{sys.implementation.cache_tag}-torch{torch.__version__}.so")
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
