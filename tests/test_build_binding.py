@@ -70,6 +70,7 @@ def test_the_built_marshalling_is_loaded(build):
 def test_another_torch_or_python_builds_anew(build, monkeypatch, what):
     assert os.path.exists(build.binding_path())
     ran = []
+    monkeypatch.setattr(build.os.path, "getmtime", lambda f: 0.0)     # all of one age
     monkeypatch.setattr(build.subprocess, "run", lambda cmd, check: ran.append(cmd))
     monkeypatch.setattr(build.os, "replace", lambda a, b: ran.append((a, b)))
     old = build.build_binding()
